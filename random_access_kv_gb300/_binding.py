@@ -1,4 +1,5 @@
-"""ctypes binding of libfq.so: the C ABI of include/fq.h and include/fractal.h under the same names.
+"""ctypes binding of libfq.so: the C ABI of include/fq.h, include/fractal.h and include/qcache.h under
+the same names.
 
 Argument marshalling only: every function takes device buffers as torch CUDA tensors (or raw
 integer addresses), passes their addresses and sizes to the C entry point of the same name and
@@ -15,11 +16,13 @@ import re
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfq.so")
-HEADERS = [os.path.join(os.path.dirname(PKG), "include", h) for h in ("fq.h", "fractal.h")]
+HEADERS = [os.path.join(os.path.dirname(PKG), "include", h) for h in ("fq.h", "fractal.h", "qcache.h")]
 
 FQ_OK, FQ_EINVAL, FQ_ENOMEM, FQ_ECUDA, FQ_EALIGN, FQ_ENODEV = range(6)
 FQ_FLAG_RANGE, FQ_FLAG_NONFINITE, FQ_FLAG_TIMEOUT = 1, 2, 4
 FA_FLAG_SYMBOL, FA_FLAG_RANGE, FA_FLAG_CORRUPT = 1, 2, 4
+QC_FORMATS = {"int8": 0, "e4m3": 1, "e2m1": 2}
+QC_FLAG_RANGE, QC_FLAG_NONFINITE, QC_FLAG_TIMEOUT = 1, 2, 4
 
 
 class FQLibraryMissing(ImportError):
@@ -62,18 +65,32 @@ _SIGNATURES = {
     "fa_access": (_int, [_c_void_p, _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p, _c_void_p]),
     "fa_status": (_int, [_c_void_p, _c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
     "fa_destroy": (None, [_c_void_p]),
+    "qc_create": (_int, [ctypes.POINTER(_c_void_p), _int, _int, _int, _int, _int]),
+    "qc_page_bytes": (_i64, [_c_void_p]),
+    "qc_norm_rope": (_int, [_c_void_p, _int, _i64, _c_void_p, _int, _i64, _i64, _c_void_p, _c_void_p, _int, _i64, _i64,
+                            _c_void_p, ctypes.c_float, _c_void_p, _c_void_p, _i64, _int, _int, _c_void_p, _i64, _i64,
+                            _c_void_p, _i64, _i64, _c_void_p]),
+    "qc_write": (_int, [_c_void_p, _int, _i64, _c_void_p, _i64, _i64, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i64,
+                        _c_void_p]),
+    "qc_read": (_int, [_c_void_p, _int, _i64, _c_void_p, _c_void_p, _i64, _c_void_p, _c_void_p, _c_void_p]),
+    "qc_attend": (_int, [_c_void_p, _int, _i64, _int, _int, _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _c_void_p,
+                         _c_void_p, _c_void_p, _c_void_p, _i64, ctypes.c_float, _i64, _c_void_p, _c_void_p, _c_void_p,
+                         _i64, _c_void_p]),
+    "qc_attend_workspace": (_i64, [_c_void_p, _i64, _int, _int, _i64]),
+    "qc_status": (_int, [_c_void_p, _c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
+    "qc_destroy": (None, [_c_void_p]),
 }
 
 _lib = None
 
 
 def header_symbols() -> list[str]:
-    """Names of the functions declared in include/fq.h and include/fractal.h."""
+    """Names of the functions declared in the headers under include/."""
     names = set()
     for h in HEADERS:
         with open(h) as f:
             text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
-        names.update(re.findall(r"\b((?:fq|fa)_[a-z0-9_]+)\s*\(", text))
+        names.update(re.findall(r"\b((?:fq|fa|qc)_[a-z0-9_]+)\s*\(", text))
     return sorted(names)
 
 
@@ -301,4 +318,192 @@ def fa_status(ctx: ArchiveContext, stream=None) -> int:
 
 
 def fa_destroy(ctx: ArchiveContext) -> None:
+    ctx.close()
+
+
+# Paged cache of quantised keys and values (include/qcache.h).
+
+class CacheContext(Context):
+    """Owns a ``qc_ctx*`` and knows its geometry; frees it with ``qc_destroy``."""
+
+    _destroy = "qc_destroy"
+
+    def __init__(self, handle: int, fmt: str, d: int, n_heads: int, page_tokens: int, device: int):
+        super().__init__(handle)
+        self.fmt, self.d, self.n_heads, self.page_tokens, self.device = fmt, d, n_heads, page_tokens, device
+        self._as_parameter_cached = ctypes.c_void_p(handle)
+
+    @property
+    def _as_parameter_(self):
+        return self._as_parameter_cached
+
+    def close(self) -> None:
+        super().close()
+        self._as_parameter_cached = ctypes.c_void_p(0)
+
+
+_qc_types = {}
+
+
+def _qc_type(t) -> int:
+    """QC_* code of a tensor's element type."""
+    if not _qc_types:
+        import torch
+        _qc_types.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    code = _qc_types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"rows are float16, bfloat16 or float32, not {t.dtype}")
+    return code
+
+
+def _want(t, what: str, ctx: CacheContext, dtype=None, shape=None) -> None:
+    """Refuses what the C call could not see: another device, type or shape, an inner stride, too few rows."""
+    if t.device.index != ctx.device or t.device.type != "cuda":
+        raise ValueError(f"{what} is on {t.device}, the context on cuda:{ctx.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} is {t.dtype}, not {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} is {tuple(t.shape)}, not {shape}")
+
+
+def _want_flat(t, what: str, ctx: CacheContext, dtype, shape=None) -> None:
+    _want(t, what, ctx, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{what} is not contiguous")
+
+
+def _want_heads(t, what: str, ctx: CacheContext, dtype, n: int | None = None, heads: int | None = None) -> None:
+    _want(t, what, ctx, dtype)
+    s = t.shape
+    if len(s) != 3 or s[2] != ctx.d or (n is not None and s[0] != n) or (heads is not None and s[1] != heads):
+        raise ValueError(f"{what} is {tuple(s)}, not [{'n' if n is None else n}, {'heads' if heads is None else heads}, {ctx.d}]")
+    if t.stride(2) != 1:
+        raise ValueError(f"{what}: the elements of a row are not next to each other")
+
+
+def _want_pages(pages, ctx: CacheContext) -> int:
+    import torch
+    _want_flat(pages, "pages", ctx, torch.uint8)
+    if pages.dim() != 2 or pages.shape[1] != qc_page_bytes(ctx):
+        raise ValueError(f"pages is {tuple(pages.shape)}, not [n_pages, {qc_page_bytes(ctx)}]")
+    return pages.shape[0]
+
+
+def qc_create(fmt: str, d: int, n_heads: int, page_tokens: int, device: int = 0) -> CacheContext:
+    """fmt: "int8", "e4m3" or "e2m1"."""
+    if fmt not in QC_FORMATS:
+        raise ValueError(f"fmt is one of {sorted(QC_FORMATS)}, not {fmt!r}")
+    h = _c_void_p()
+    _check("qc_create", lib().qc_create(ctypes.byref(h), QC_FORMATS[fmt], int(d), int(n_heads), int(page_tokens), int(device)))
+    return CacheContext(h.value, fmt, int(d), int(n_heads), int(page_tokens), int(device))
+
+
+def qc_page_bytes(ctx: CacheContext) -> int:
+    b = lib().qc_page_bytes(ctx)
+    if b < 0:
+        raise FQError("qc_page_bytes", FQ_EINVAL)
+    return int(b)
+
+
+def qc_norm_rope(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, rot: int, interleaved: bool, q_out, k_out,
+                 stream=None) -> None:
+    """q [n, hq, d] and k [n, hk, d] (either may be None), strided; w_q, w_k float32 [d] or None; pos int64
+    [n]; table float32 [max_pos, rot]; q_out, k_out like q and k (themselves, too)."""
+    import torch
+    args, n, dtype, max_pos = [], None, None, 0
+    for x, out, w, name in ((q, q_out, w_q, "q"), (k, k_out, w_k, "k")):
+        if x is None:
+            args.append((None, 0, 0, 0, None, None, 0, 0))
+            continue
+        dtype = x.dtype if dtype is None else dtype
+        _want_heads(x, name, ctx, dtype, n)
+        n = x.shape[0]
+        _want_heads(out, name + "_out", ctx, dtype, n, x.shape[1])
+        if w is not None:
+            _want_flat(w, "w_" + name, ctx, torch.float32, (ctx.d,))
+        args.append((_ptr(x), x.shape[1], x.stride(0), x.stride(1), _ptr(w), _ptr(out), out.stride(0), out.stride(1)))
+    if n is None:
+        raise ValueError("neither q nor k")
+    if rot:
+        _want_flat(pos, "pos", ctx, torch.int64, (n,))
+        _want_flat(table, "table", ctx, torch.float32, (table.shape[0], rot))
+        max_pos = table.shape[0]
+    a, b = args
+    _check("qc_norm_rope", lib().qc_norm_rope(ctx, _qc_type(q if q is not None else k), n, *a[:5], *b[:5], eps,
+                                              _ptr(pos) if rot else None, _ptr(table) if rot else None, max_pos, rot,
+                                              interleaved, *a[5:], *b[5:], _stream(stream)))
+
+
+def qc_write(ctx: CacheContext, k, v, slots, pages, stream=None) -> None:
+    """k, v [n, n_heads, d], strided; slots int64 [n]; pages uint8 [n_pages, qc_page_bytes(ctx)]."""
+    import torch
+    n = k.shape[0]
+    _want_heads(k, "k", ctx, k.dtype, n, ctx.n_heads)
+    _want_heads(v, "v", ctx, k.dtype, n, ctx.n_heads)
+    _want_flat(slots, "slots", ctx, torch.int64, (n,))
+    n_pages = _want_pages(pages, ctx)
+    _check("qc_write", lib().qc_write(ctx, _qc_type(k), n, _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+                                      v.stride(1), _ptr(slots), _ptr(pages), n_pages, _stream(stream)))
+
+
+def qc_read(ctx: CacheContext, pages, slots, k_out, v_out, stream=None) -> None:
+    """slots int64 [n]; k_out, v_out [n, n_heads, d], contiguous, or None."""
+    import torch
+    n, n_pages = slots.shape[0], _want_pages(pages, ctx)
+    _want_flat(slots, "slots", ctx, torch.int64, (n,))
+    out = k_out if k_out is not None else v_out
+    if out is None:
+        return
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _want_flat(t, name, ctx, out.dtype, (n, ctx.n_heads, ctx.d))
+    _check("qc_read", lib().qc_read(ctx, _qc_type(out), n, _ptr(slots), _ptr(pages), n_pages, _ptr(k_out), _ptr(v_out),
+                                    _stream(stream)))
+
+
+def qc_attend(ctx: CacheContext, pages, q, table, lens, nodes, tree, scale: float, max_len: int, out, lse, workspace,
+              stream=None) -> None:
+    """q [n_seq, n_nodes, n_q_heads, d], strided; table int32 [n_seq, >= places / page_tokens]; lens, nodes int32
+    [n_seq] (nodes may be None); tree int32 [n_seq, n_nodes, ceil(n_nodes / 32)] or None; out like q,
+    contiguous; lse float32 [n_seq, n_nodes, n_q_heads] or None; workspace from alloc_attend_workspace."""
+    import torch
+    if q.dim() != 4 or q.shape[3] != ctx.d or q.stride(3) != 1:
+        raise ValueError(f"q is {tuple(q.shape)}, not [n_seq, n_nodes, n_q_heads, {ctx.d}] with its rows' elements together")
+    n_seq, n_nodes, hq, _ = q.shape
+    n_pages = _want_pages(pages, ctx)
+    _want(q, "q", ctx)
+    _want_flat(out, "out", ctx, q.dtype, (n_seq, n_nodes, hq, ctx.d))
+    _want(table, "table", ctx, torch.int32)
+    if table.dim() != 2 or table.shape[0] != n_seq or (table.stride(1) != 1 and table.shape[1] > 1):
+        raise ValueError(f"table is {tuple(table.shape)}, not [{n_seq}, pages per sequence] with rows of their own")
+    if -(-(max_len + n_nodes) // ctx.page_tokens) > table.shape[1]:
+        raise FQError("qc_attend", FQ_EINVAL)
+    _want_flat(lens, "lens", ctx, torch.int32, (n_seq,))
+    if nodes is not None:
+        _want_flat(nodes, "nodes", ctx, torch.int32, (n_seq,))
+    if tree is not None:
+        _want_flat(tree, "tree", ctx, torch.int32, (n_seq, n_nodes, (n_nodes + 31) // 32))
+    if lse is not None:
+        _want_flat(lse, "lse", ctx, torch.float32, (n_seq, n_nodes, hq))
+    _want_flat(workspace, "workspace", ctx, torch.uint8)
+    _check("qc_attend", lib().qc_attend(ctx, _qc_type(q), n_seq, n_nodes, hq, _ptr(q), q.stride(0), q.stride(1), q.stride(2),
+                                        _ptr(table), table.stride(0), _ptr(lens), _ptr(nodes), _ptr(tree), _ptr(pages),
+                                        n_pages, scale, max_len, _ptr(out), _ptr(lse), _ptr(workspace),
+                                        workspace.numel(), _stream(stream)))
+
+
+def qc_attend_workspace(ctx: CacheContext, n_seq: int, n_nodes: int, n_q_heads: int, max_len: int) -> int:
+    b = lib().qc_attend_workspace(ctx, int(n_seq), int(n_nodes), int(n_q_heads), int(max_len))
+    if b < 0:
+        raise FQError("qc_attend_workspace", FQ_EINVAL)
+    return int(b)
+
+
+def qc_status(ctx: CacheContext, stream=None) -> int:
+    f = ctypes.c_uint32()
+    _check("qc_status", lib().qc_status(ctx, _stream(stream), ctypes.byref(f)))
+    return int(f.value)
+
+
+def qc_destroy(ctx: CacheContext) -> None:
     ctx.close()
