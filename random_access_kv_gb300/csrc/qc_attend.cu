@@ -1,99 +1,89 @@
-// Attention of drafted tokens over the quantised cache: one warp per query row.
-//
-// A lane holds d / 32 elements of the query; every place that the row sees costs one dot product over
-// the warp, one step of the running maximum and sum, and d / 32 multiply-adds per lane.
+// Attention over the quantised cache: choice of the kernel, and the joining of the parts that it leaves.
 #include <math.h>
 
-#include "qc_formats.cuh"
+#include "qc_attend.cuh"
 
 namespace qc {
 namespace {
 
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
-template <int FMT>
-__device__ __forceinline__ float element(const Geometry &g, const unsigned char *part, int which, int t, int e) {
-    const int byte = t * g.row + (FMT == QC_E2M1 ? e / 2 : e);
-    const uint32_t c = part[g.codes(which) + piece_at(byte >> 4) * 16 + (byte & 15)];
-    if constexpr (FMT == QC_INT8) return (float)(signed char)c;
-    if constexpr (FMT == QC_E4M3) return e4m3_value(c);
-    const uint32_t h = half2_e2m1(e & 1 ? c >> 4 : c & 15u);
-    const float sb = e4m3_value(part[g.block_scales(which) + t * g.blocks + e / 16]);
-    return __half2float(__ushort_as_half((unsigned short)h)) * 16384.f * sb;
-}
-
-template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreads) attend(const Attend p) {
-    constexpr int E = D / 32;
+// One warp per query row. Rows of jobs within one CTA are done already; the others' parts lie in
+// consecutive CTAs: part 2 c + 1 of the first (part 2 c if the job begins its run), part 2 c of the rest.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) join_parts(const Attend p, const Parts parts, int row_tiles, int tile, int ctas) {
+    fq::sm100::griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (row >= (int64_t)p.n_seq * p.n_nodes * p.n_q_heads) return;
-    const int head = (int)(row % p.n_q_heads), node = (int)(row / p.n_q_heads % p.n_nodes);
-    const int b = (int)(row / p.n_q_heads / p.n_nodes), kv = head / p.group;
-    int len = p.lens[b], nodes = p.nodes ? p.nodes[b] : p.n_nodes;
-    if (len < 0 || len > p.max_len || nodes < 0 || nodes > p.n_nodes) {
-        if (lane == 0) atomicOr(p.flags, QC_FLAG_RANGE);
-        len = min(max(len, 0), (int)p.max_len);
-        nodes = min(max(nodes, 0), p.n_nodes);
-    }
-    const T *q = static_cast<const T *>(p.q) + b * p.q_seq + node * p.q_node + head * p.q_head;
-    float qv[E], o[E];
-    for (int i = 0; i < E; ++i) qv[i] = to_float(q[i * 32 + lane]), o[i] = 0.f;
+    const int R = p.n_nodes * p.group;
+    if (row >= (int64_t)p.n_seq * p.g.heads * R) return;
+    const int r = (int)(row % R), h = (int)(row / R % p.g.heads), b = (int)(row / R / p.g.heads);
+    const int jobs = p.g.heads * row_tiles, rt = r / parts.rows, rr = r - rt * parts.rows;
+    const int2 n = lengths(p, b, false);
+    const int tiles = tiles_of(n, tile);
+    const int64_t out_row = ((int64_t)b * p.n_nodes + r / p.group) * p.n_q_heads + h * p.group + r % p.group;
     float m = -INFINITY, l = 0.f;
-    const uint32_t *tree = p.tree ? p.tree + ((int64_t)b * p.n_nodes + node) * p.words : nullptr;
-    const int end = node < nodes ? len + nodes : 0;
-    for (int t = 0; t < end; ++t) {
-        if (t >= len) {
-            const int j = t - len;
-            if (tree ? !((tree[j >> 5] >> (j & 31)) & 1u) : j > node) continue;
+    float o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+    if (tiles && r / p.group < n.y) {
+        const int64_t before = parts.before[b], total = parts.before[p.n_seq];
+        const int64_t per = run_length(total, ctas);
+        const int64_t first = before + (int64_t)(h * row_tiles + rt) * tiles;
+        const int64_t c0 = first / per, c1 = (first + tiles - 1) / per;
+        if (c0 == c1) return;
+        const int64_t p0 = 2 * c0 + (first == c0 * per ? 0 : 1);
+        for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, parts.stat(c == c0 ? p0 : 2 * c, rr)->x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        for (int64_t c = c0; c <= c1; ++c) {
+            const int64_t at = c == c0 ? p0 : 2 * c;
+            const float2 s = *parts.stat(at, rr);
+            const float w = exp2f(s.x - ref);
+            l = fmaf(s.y, w, l);
+            const float *v = parts.row(at, rr) + lane * (D / 32);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(v[i], w, o[i]);
         }
-        const int64_t page = p.table[b * p.table_stride + (t >> p.g.shift)];
-        if (page < 0 || page >= p.n_pages) {
-            if (lane == 0) atomicOr(p.flags, QC_FLAG_RANGE);
-            continue;
-        }
-        const unsigned char *part = p.pages + (page * p.g.heads + kv) * (int64_t)p.g.part;
-        const int at = t & (p.g.page - 1);
-        float s = 0.f;
-        for (int i = 0; i < E; ++i) s += qv[i] * element<FMT>(p.g, part, 0, at, i * 32 + lane);
-        for (int x = 16; x >= 1; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= reinterpret_cast<const float *>(part + p.g.scales(0))[at] * p.scale;
-        const float m2 = fmaxf(m, s), w = expf(s - m2), old = expf(m - m2);
-        const float vs = reinterpret_cast<const float *>(part + p.g.scales(1))[at] * w;
-        l = l * old + w;
-        for (int i = 0; i < E; ++i) o[i] = o[i] * old + vs * element<FMT>(p.g, part, 1, at, i * 32 + lane);
-        m = m2;
     }
-    T *out = static_cast<T *>(p.out) + row * D;
-    for (int i = 0; i < E; ++i) put(out + i * 32 + lane, l > 0.f ? o[i] / l : 0.f);
-    if (p.lse && lane == 0) p.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    T *out = static_cast<T *>(p.out) + out_row * D + lane * (D / 32);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] *= inv;
+    store_row<T, D / 32>(out, o);
+    if (p.lse && lane == 0) p.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <typename T, int D>
-cudaError_t launch(const qc_ctx *c, const Attend &p, cudaStream_t s) {
-    const int64_t rows = (int64_t)p.n_seq * p.n_nodes * p.n_q_heads, blocks = (rows + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    if (c->fmt == QC_INT8)
-        attend<T, D, QC_INT8><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    else if (c->fmt == QC_E4M3)
-        attend<T, D, QC_E4M3><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    else
-        attend<T, D, QC_E2M1><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+cudaError_t join(const Attend &p, const Parts &parts, int row_tiles, int tile, int ctas, cudaStream_t s) {
+    const int64_t rows = (int64_t)p.n_seq * p.n_nodes * p.n_q_heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_parts<T, D>, p, parts, row_tiles, tile, ctas);
 }
 
 }  // namespace
 
-int64_t attend_workspace(const qc_ctx *, int64_t, int, int, int64_t) { return 0; }
+cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int ctas, cudaStream_t s) {
+    if (type == QC_F16)
+        return p.g.d == 64 ? join<__half, 64>(p, parts, row_tiles, tile, ctas, s)
+                           : join<__half, 128>(p, parts, row_tiles, tile, ctas, s);
+    return p.g.d == 64 ? join<__nv_bfloat16, 64>(p, parts, row_tiles, tile, ctas, s)
+                       : join<__nv_bfloat16, 128>(p, parts, row_tiles, tile, ctas, s);
+}
+
+int64_t attend_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {
+    return rows_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
+}
 
 cudaError_t launch_attend(const qc_ctx *c, int type, const Attend &p, cudaStream_t s) {
-    if (type == QC_F16) return c->d == 64 ? launch<__half, 64>(c, p, s) : launch<__half, 128>(c, p, s);
-    return c->d == 64 ? launch<__nv_bfloat16, 64>(c, p, s) : launch<__nv_bfloat16, 128>(c, p, s);
+    return launch_attend_rows(c, type, p, s);
 }
 
 }  // namespace qc
