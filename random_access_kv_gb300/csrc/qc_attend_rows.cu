@@ -1,10 +1,11 @@
 // Attention over the quantised cache for few query rows per key/value head (single tokens, chains,
 // small trees).
 //
-// What bounds it: the pages, read once. A producer warp copies tiles of 64 places from the pages, as
-// they lie, to a ring of shared-memory stages with bulk asynchronous copies (one per page part, so the
-// copies of several tiles are under way at any time); the consumer warps turn codes into tensor-core
-// fragments in registers.
+// What bounds it: the pages, read once. Every warp is a CTA of its own, eight on an SM, with a run of
+// tiles of 32 places. It copies them from the pages, as they lie, to its ring of shared-memory stages
+// with bulk asynchronous copies, two or more tiles ahead, and turns codes into tensor-core fragments in
+// registers. Warps never wait for one another; what one leaves unused of the memory's bandwidth, for
+// instance at the start of a job, the other seven on its SM take.
 //
 // Products. Codes are exact in fp16, and so are e2m1 codes times their e4m3 block scale (5 bits), so
 // the products q . code are exact and summed in float32; the row's scale multiplies the score
@@ -27,13 +28,13 @@ namespace {
 
 using namespace fq::sm100;
 
-constexpr int kTile = 64;               // places per stage
-constexpr int kSlices = 4;              // warps that share a stage, 16 places each
-constexpr int kRows = 16;               // query rows of a warp
+constexpr int kTile = 32;               // places per stage
+constexpr int kPerSm = 8;               // CTAs (warps) on an SM: 255 registers and 27 KB each
+constexpr int kRoom = 27 * 1024;
 constexpr float kWeight = 16384.f;      // 2^14
 constexpr float kLeastNormal = 6.103515625e-05f;    // 2^-14, fp16's
 constexpr float kLift = 16777216.f;     // 2^24
-constexpr float kThin = 16.f;           // a quarter of a row's sum of weights, the heaviest being 1
+constexpr float kThin = 2.f;            // about a quarter of a row's sum of weights, the heaviest being 1
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -78,7 +79,9 @@ struct Shape {
     static constexpr int kRow = FMT == QC_E2M1 ? D / 2 : D;             // bytes of a row's codes
     static constexpr int kBlocks = FMT == QC_E2M1 ? D / 16 : 0;
     static constexpr int kStage = 2 * kTile * (kRow + 4 + kBlocks);     // bytes of a tile
-    // Place (0 .. 15 of a slice) of column n of 8-wide score tile u.
+    // A stage: keys' codes, values' codes, keys' scales, values' scales, keys' block scales, values'.
+    static constexpr int kCodes = kTile * kRow, kScales = 2 * kCodes, kBlockScales = kScales + 8 * kTile;
+    // Place (0 .. 15 of a half tile) of column n of 8-wide score tile u.
     static __device__ __forceinline__ int place(int u, int n) {
         if constexpr (kRow == 128) return 8 * u + n;
         if constexpr (kRow == 64) return 4 * (n >> 1) + 2 * u + (n & 1);
@@ -87,56 +90,47 @@ struct Shape {
 };
 
 struct Plan {
-    int row_tiles;      // tiles of `rows` rows per head
-    int row_warps;      // warps' row tiles of 16 in a CTA (1 or 2)
+    int row_tiles;      // tiles of 16 MT rows per head
+    int mt;             // 16-row tiles of a warp (1 or 2)
     int stages;
     int ctas;
     int smem;
 };
 
-struct Shared {
-    uint64_t full[16], empty[16];
-    uint32_t bad[16];           // per stage: sixteenths of the tile whose page does not exist
-    Walk start;
-    uint32_t fail;
-};
-
-// One thread's share of a slice's offsets within a stage.
+// One lane's offsets within a stage. Rows of 128 and 64 bytes: the other offsets are these plus
+// constants; rows of 32 bytes: the swizzle's phase differs between half tiles.
 template <int FMT, int D>
 struct Offsets {
     using S = Shape<FMT, D>;
-    int k[2][S::kRow == 128 ? 2 : 1];   // keys' codes: of column g of tile u
-    int v[4];                           // values' codes: of the lane's four places
-    int ks[4], vs[4];                   // scales of the lane's four places
-    int kb[2], vb[4];                   // block scales
-    __device__ __forceinline__ void set(int slice, int page, int g, int c) {
-        const int sub_tokens = page < kTile ? page : kTile;
-        const int t0 = slice * 16, base = t0 / sub_tokens * (2 * sub_tokens * (S::kRow + 4 + S::kBlocks)), at = t0 % sub_tokens;
-        const int vcodes = base + sub_tokens * S::kRow, scales = base + 2 * sub_tokens * S::kRow;
-        const int blocks = scales + 8 * sub_tokens;
+    static constexpr int kK = S::kRow == 128 ? 1 : S::kRow == 64 ? 2 : 4, kV = 2 * kK;
+    int k[kK], v[kV];
+    static __device__ __forceinline__ int code(int t, int byte, bool short_pages) {
+        byte += t * S::kRow;
+        if (S::kRow == 32 && short_pages && t >= 16)        // a page of 16 begins its own run
+            return 16 * S::kRow + piece_at((byte - 16 * S::kRow) >> 4) * 16 + (byte & 15);
+        return piece_at(byte >> 4) * 16 + (byte & 15);
+    }
+    __device__ __forceinline__ void set(int g, int c, bool short_pages) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int t = at + S::place(u, g);
+        for (int i = 0; i < kK; ++i) k[i] = code(16 * (i >> 1) + S::place(i & 1, g), c * (S::kRow / 4), short_pages);
 #pragma unroll
-            for (int h = 0; h < (S::kRow == 128 ? 2 : 1); ++h) {
-                const int byte = t * S::kRow + c * (S::kRow / 4) + 16 * h;
-                k[u][h] = base + piece_at(byte >> 4) * 16 + (byte & 15);
-            }
-            kb[u] = blocks + t * S::kBlocks + c * (S::kBlocks / 4);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int tv = at + S::place(u, 2 * c + e), byte = tv * S::kRow + g * (S::kRow / 8);
-                v[2 * u + e] = vcodes + piece_at(byte >> 4) * 16 + (byte & 15);
-                ks[2 * u + e] = scales + tv * 4;
-                vs[2 * u + e] = scales + (sub_tokens + tv) * 4;
-                vb[2 * u + e] = blocks + (sub_tokens + tv) * S::kBlocks + g * S::kBlocks / 8;
-            }
-        }
+        for (int i = 0; i < kV; ++i)
+            v[i] = S::kCodes + code(16 * (i >> 2) + S::place(S::kRow == 128 ? 0 : (i >> 1) & 1, 2 * c + (i & 1)), g * (S::kRow / 8), short_pages);
+    }
+    __device__ __forceinline__ int key(int x, int u, int h) const {
+        if constexpr (S::kRow == 128) return (k[0] ^ (16 * h)) + 1024 * u + 2048 * x;
+        if constexpr (S::kRow == 64) return k[u] + 1024 * x;
+        return k[2 * x + u];
+    }
+    __device__ __forceinline__ int value(int x, int u, int e) const {
+        if constexpr (S::kRow == 128) return v[e] + 1024 * u + 2048 * x;
+        if constexpr (S::kRow == 64) return v[2 * u + e] + 1024 * x;
+        return v[4 * x + 2 * u + e];
     }
 };
 
 template <int N>
-__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)[N]) {
+__device__ __forceinline__ void load_words(const unsigned char *p, uint32_t *w) {
     if constexpr (N == 4) {
         const uint4 r = *reinterpret_cast<const uint4 *>(p);
         w[0] = r.x, w[1] = r.y, w[2] = r.z, w[3] = r.w;
@@ -148,41 +142,188 @@ __device__ __forceinline__ void load_words(const unsigned char *p, uint32_t (&w)
     }
 }
 
-// Scores of the slice: s[u][e] row g, s[u][2 + e] row g + 8, place(u, 2 c + e), before any scale.
-template <int FMT, int D>
-__device__ __forceinline__ void scores(const unsigned char *st, const Offsets<FMT, D> &o, const uint32_t (&qa)[D / 16][4],
-                                       float (&s)[2][4]) {
+// The scales of the lane's eight places: [4 x + 2 u + e] is that of place(u, 2 c + e) of half tile x.
+template <int ROW>
+__device__ __forceinline__ void load_scales(const unsigned char *p, int c, float (&s)[8]) {
+    const float *f = reinterpret_cast<const float *>(p);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        if constexpr (ROW == 128) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float2 r = *reinterpret_cast<const float2 *>(f + 16 * x + 8 * u + 2 * c);
+                s[4 * x + 2 * u] = r.x;
+                s[4 * x + 2 * u + 1] = r.y;
+            }
+        } else if constexpr (ROW == 64) {
+            const float4 r = *reinterpret_cast<const float4 *>(f + 16 * x + 4 * c);
+            s[4 * x] = r.x, s[4 * x + 1] = r.y, s[4 * x + 2] = r.z, s[4 * x + 3] = r.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[4 * x + i] = f[16 * x + c + 4 * i];
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t sub1152(uint32_t x) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Query fragments: in registers for one row tile; for two in shared memory, lane by lane.
+template <int D, int MT>
+struct Queries;
+template <int D>
+struct Queries<D, 1> {
+    uint32_t a[D / 16][4];
+    __device__ __forceinline__ void put(uint4 *, int, int, int i, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        a[i][0] = w0, a[i][1] = w1, a[i][2] = w2, a[i][3] = w3;
+    }
+    __device__ __forceinline__ void get(const uint4 *, int, int, int i, uint32_t (&r)[4]) const {
+        r[0] = a[i][0], r[1] = a[i][1], r[2] = a[i][2], r[3] = a[i][3];
+    }
+};
+template <int D>
+struct Queries<D, 2> {
+    __device__ __forceinline__ void put(uint4 *sm, int lane, int mt, int i, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        sm[(mt * (D / 16) + i) * 32 + lane] = make_uint4(w0, w1, w2, w3);
+    }
+    __device__ __forceinline__ void get(const uint4 *sm, int lane, int mt, int i, uint32_t (&r)[4]) const {
+        const uint4 v = sm[(mt * (D / 16) + i) * 32 + lane];
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    }
+};
+
+// Scores of a tile before any scale: s[mt][2 x + u][2 r + e] of row g + 8 r, place(u, 2 c + e) of half x.
+template <int FMT, int D, int MT>
+__device__ __forceinline__ void scores(const unsigned char *st, const Offsets<FMT, D> &o, const Queries<D, MT> &q, const uint4 *qs,
+                                       int lane, float (&s)[MT][4][4]) {
     using S = Shape<FMT, D>;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][i] = 0.f;
+        for (int n = 0; n < 4; ++n) s[m][n][0] = s[m][n][1] = s[m][n][2] = s[m][n][3] = 0.f;
+    constexpr int kChunks = S::kRow == 128 ? 2 : 1, kWords = S::kRow / 16 / kChunks;     // a lane's words per place
+    constexpr int kSteps = FMT == QC_E2M1 ? 2 : 1;                                       // 16-wide steps per word
+#pragma unroll
+    for (int h = 0; h < kChunks; ++h) {
+        uint32_t w[4][kWords];
+        uint32_t sb[4][2];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            load_words<kWords>(st + o.key(n >> 1, n & 1, h), w[n]);
+            if constexpr (FMT == QC_E2M1) {
+                const unsigned char *b = st + S::kBlockScales + (16 * (n >> 1) + S::place(n & 1, lane >> 2)) * S::kBlocks + (lane & 3) * (S::kBlocks / 4);
+                if constexpr (D == 128) {
+                    const uint32_t x = *reinterpret_cast<const uint16_t *>(b);
+                    sb[n][0] = cvt_e4m3(__byte_perm(x, 0, 0x4400));
+                    sb[n][1] = cvt_e4m3(__byte_perm(x, 0, 0x4411));
+                } else {
+                    sb[n][0] = both_e4m3(*b);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            uint32_t qa[MT][kSteps][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) q.get(qs, lane, m, (h * kWords + i) * kSteps + k, qa[m][k]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                uint32_t b[4];
+                if constexpr (FMT == QC_E2M1) {
+                    cvt_e2m1(w[n][i], b);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) b[j] = mul2(b[j], sb[n][i / 2]);
+                } else if constexpr (FMT == QC_INT8) {
+                    const uint32_t x = w[n][i] ^ 0x80808080u;
+                    b[0] = sub1152(__byte_perm(x, 0x64646464u, 0x4140));
+                    b[1] = sub1152(__byte_perm(x, 0x64646464u, 0x4342));
+                } else {
+                    b[0] = cvt_e4m3(w[n][i]);
+                    b[1] = cvt_e4m3(w[n][i] >> 16);
+                }
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma(s[m][n], qa[m][k], b[2 * k], b[2 * k + 1]);
+            }
+        }
+    }
+}
+
+// out[mt][nt] += weights a[mt][x] times the values of half tile x. keep: which of the lane's eight places
+// exist (only asked when MASK; the others' bytes may be anything, NaN codes included, and count as zeros).
+template <int FMT, int D, int MT, bool MASK>
+__device__ __forceinline__ void add_values(const unsigned char *st, const Offsets<FMT, D> &o, const uint32_t (&a)[MT][2][4], int lane,
+                                           uint32_t keep, float (&out)[MT][D / 8][4]) {
+    using S = Shape<FMT, D>;
+    constexpr int W = S::kRow / 32;                     // words of a place in a lane
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        uint32_t w[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            load_words<W>(st + o.value(x, i >> 1, i & 1), w[i]);
+            if (MASK && !((keep >> (4 * x + i)) & 1u)) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[i][j] = 0;
+            }
+        }
         if constexpr (FMT == QC_E2M1) {
-            uint32_t w[D / 32];
-            load_words(st + o.k[u][0], w);
-            uint32_t sb[D / 64];
+            uint32_t sb[2];
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) sb[i] = both_e4m3(st[o.kb[u] + i]);
+            for (int i = 0; i < 2; ++i) {
+                const unsigned char *b = st + S::kBlockScales + kTile * S::kBlocks + (lane >> 2) * S::kBlocks / 8;
+                uint32_t y = b[(16 * x + S::place(i, 2 * (lane & 3))) * S::kBlocks], z = b[(16 * x + S::place(i, 2 * (lane & 3) + 1)) * S::kBlocks];
+                if (MASK && !((keep >> (4 * x + 2 * i)) & 1u)) y = 0;
+                if (MASK && !((keep >> (4 * x + 2 * i + 1)) & 1u)) z = 0;
+                sb[i] = cvt_e4m3(y | z << 8);
+            }
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t h[4];
-                cvt_e2m1(w[i], h);
-                mma(s[u], qa[2 * i], mul2(h[0], sb[i / 2]), mul2(h[1], sb[i / 2]));
-                mma(s[u], qa[2 * i + 1], mul2(h[2], sb[i / 2]), mul2(h[3], sb[i / 2]));
+            for (int j = 0; j < W; ++j) {
+                uint32_t h[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cvt_e2m1(w[i][j], h[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
+                    const uint32_t b0 = mul2(__byte_perm(h[0][e / 2], h[1][e / 2], sel), sb[0]);
+                    const uint32_t b1 = mul2(__byte_perm(h[2][e / 2], h[3][e / 2], sel), sb[1]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma(out[m][8 * j + e], a[m][x], b0, b1);
+                }
             }
         } else {
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                uint32_t w[4];
-                load_words(st + o.k[u][h], w);
+            for (int j = 0; j < W; ++j) {
+                if constexpr (FMT == QC_INT8) {
+                    // bytes of two places side by side, then fp16 pairs of (place, next place)
+                    const uint32_t y0 = __byte_perm(w[0][j], w[1][j], 0x5140) ^ 0x80808080u, y1 = __byte_perm(w[0][j], w[1][j], 0x7362) ^ 0x80808080u;
+                    const uint32_t z0 = __byte_perm(w[2][j], w[3][j], 0x5140) ^ 0x80808080u, z1 = __byte_perm(w[2][j], w[3][j], 0x7362) ^ 0x80808080u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (FMT == QC_INT8) {
-                        const uint32_t x = w[i] ^ 0x80808080u;
-                        mma(s[u], qa[4 * h + i], half2_int8(__byte_perm(x, 0x64646464u, 0x4140)),
-                            half2_int8(__byte_perm(x, 0x64646464u, 0x4342)));
-                    } else {
-                        mma(s[u], qa[4 * h + i], cvt_e4m3(w[i]), cvt_e4m3(w[i] >> 16));
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t sel = e & 1 ? 0x4342 : 0x4140;
+                        const uint32_t b0 = sub1152(__byte_perm(e < 2 ? y0 : y1, 0x64646464u, sel));
+                        const uint32_t b1 = sub1152(__byte_perm(e < 2 ? z0 : z1, 0x64646464u, sel));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) mma(out[m][4 * j + e], a[m][x], b0, b1);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) h[i] = cvt_e4m3(e ? w[i][j] >> 16 : w[i][j]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t sel = k ? 0x7632 : 0x5410;
+                            const uint32_t b0 = __byte_perm(h[0], h[1], sel), b1 = __byte_perm(h[2], h[3], sel);
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) mma(out[m][4 * j + 2 * e + k], a[m][x], b0, b1);
+                        }
                     }
                 }
             }
@@ -190,82 +331,21 @@ __device__ __forceinline__ void scores(const unsigned char *st, const Offsets<FM
     }
 }
 
-// out[nt] += weights (a) times the slice's values. keep: which of the lane's four places exist (only
-// asked when MASK; the others' bytes may be anything, NaN codes included, and count as zeros).
-template <int FMT, int D, bool MASK>
-__device__ __forceinline__ void add_values(const unsigned char *st, const Offsets<FMT, D> &o, const uint32_t (&a)[4], uint32_t keep,
-                                           float (&out)[D / 8][4]) {
-    using S = Shape<FMT, D>;
-    constexpr int W = S::kRow / 32;                     // words of a place in a lane
-    uint32_t w[4][W];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        load_words(st + o.v[i], w[i]);
-        if (MASK && !((keep >> i) & 1u)) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[i][j] = 0;
-        }
-    }
-    if constexpr (FMT == QC_E2M1) {
-        uint32_t sb[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t x = st[o.vb[2 * i]], y = st[o.vb[2 * i + 1]];
-            if (MASK && !((keep >> (2 * i)) & 1u)) x = 0;
-            if (MASK && !((keep >> (2 * i + 1)) & 1u)) y = 0;
-            sb[i] = cvt_e4m3(x | y << 8);
-        }
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            uint32_t h[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) cvt_e2m1(w[i][j], h[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                mma(out[8 * j + 2 * e], a, mul2(__byte_perm(h[0][e], h[1][e], 0x5410), sb[0]),
-                    mul2(__byte_perm(h[2][e], h[3][e], 0x5410), sb[1]));
-                mma(out[8 * j + 2 * e + 1], a, mul2(__byte_perm(h[0][e], h[1][e], 0x7632), sb[0]),
-                    mul2(__byte_perm(h[2][e], h[3][e], 0x7632), sb[1]));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-            if constexpr (FMT == QC_INT8) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i][j] ^= 0x80808080u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t pick = e | (4 + e) << 8;             // byte e of both, in the even bytes
-                    const uint32_t x = __byte_perm(w[0][j], w[1][j], pick), y = __byte_perm(w[2][j], w[3][j], pick);
-                    mma(out[4 * j + e], a, half2_int8(x & 0x00ff00ffu), half2_int8(y & 0x00ff00ffu));
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i] = cvt_e4m3(e ? w[i][j] >> 16 : w[i][j]);
-                    mma(out[4 * j + 2 * e], a, __byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
-                    mma(out[4 * j + 2 * e + 1], a, __byte_perm(h[0], h[1], 0x7632), __byte_perm(h[2], h[3], 0x7632));
-                }
-            }
-        }
-    }
-}
-
-// The softmax state of a warp's 16 rows: a thread holds rows g and g + 8.
-template <int D>
+// The softmax state of a warp's rows: a thread holds rows g and g + 8 of each row tile.
+template <int D, int MT>
 struct State {
-    float m[2], l[2];       // maximum (base-2 units), this thread's share of the sum
-    float ref;              // power of two, bound of the values' scales; 0: none yet
-    float o[D / 8][4];
+    float m[MT][2], l[MT][2];   // maximum (base-2 units), this thread's share of the sum
+    float ref;                  // power of two, bound of the values' scales; 0: none yet
+    float o[MT][D / 8][4];
     __device__ __forceinline__ void clear() {
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
         ref = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        for (int t = 0; t < MT; ++t) {
+            m[t][0] = m[t][1] = -INFINITY;
+            l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+        }
     }
 };
 
@@ -280,143 +360,165 @@ __device__ __forceinline__ float power_above(float x) {
     return b == 0 ? 0.f : __uint_as_float(min((b + 0x007fffffu) & 0xff800000u, 0x7f000000u));
 }
 
-// seen: what the lane's eight scores see, bit 4 r + 2 u + e for row g + 8 r, place(u, 2 c + e); bit 8 + 2 u + e:
-// the place exists.
-template <int FMT, int D, bool MASK>
-__device__ __forceinline__ void slice(const unsigned char *st, const Offsets<FMT, D> &of, const uint32_t (&qa)[D / 16][4],
-                                      const float (&up)[2], uint32_t seen, State<D> &z) {
-    float s[2][4];
-    scores<FMT, D>(st, of, qa, s);
-    float top[2] = {-INFINITY, -INFINITY}, vs[4], vtop = 0.f;
+// What a lane's scores see: bit 8 r + 4 x + 2 u + e of row[mt] for row g + 8 r and place(u, 2 c + e) of half
+// x; there: the places that exist.
+template <int MT>
+struct Seen {
+    uint32_t row[MT], there;
+};
+
+template <int FMT, int D, int MT, bool MASK>
+__device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<FMT, D> &of, const Queries<D, MT> &q, const uint4 *qs,
+                                         const float (&up)[MT][2], const Seen<MT> &seen, int lane, State<D, MT> &z) {
+    using S = Shape<FMT, D>;
+    float s[MT][4][4];
+    scores<FMT, D, MT>(st, of, q, qs, lane, s);
+    float ks[8], vs[8], vtop = 0.f, top[MT][2];
+    load_scales<S::kRow>(st + S::kScales, lane & 3, ks);
+    load_scales<S::kRow>(st + S::kScales + 4 * kTile, lane & 3, vs);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float ks = *reinterpret_cast<const float *>(st + of.ks[i]);
-        vs[i] = *reinterpret_cast<const float *>(st + of.vs[i]);
-        if (MASK && !((seen >> (8 + i)) & 1u)) vs[i] = 0.f;
+    for (int i = 0; i < 8; ++i) {
+        if (MASK && !((seen.there >> i) & 1u)) vs[i] = 0.f;
         vtop = fmaxf(vtop, vs[i]);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float &x = s[i >> 1][2 * r + (i & 1)];
-            x *= ks * up[r];
-            if (MASK && !((seen >> (4 * r + i)) & 1u)) x = -INFINITY;
-            top[r] = fmaxf(top[r], x);
-        }
     }
     vtop = quad_max(vtop);
-    top[0] = quad_max(top[0]);
-    top[1] = quad_max(top[1]);
-    if (__any_sync(0xffffffffu, top[0] > z.m[0] || top[1] > z.m[1] || vtop > z.ref)) {
+    bool grows = vtop > z.ref;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float &y = s[t][i >> 1][2 * r + (i & 1)];
+                y *= ks[i] * up[t][r];
+                if (MASK && !((seen.row[t] >> (8 * r + i)) & 1u)) y = -INFINITY;
+                x = fmaxf(x, y);
+            }
+            top[t][r] = quad_max(x);
+            grows |= top[t][r] > z.m[t][r];
+        }
+    }
+    if (__any_sync(0xffffffffu, grows)) {
         const float ref = fmaxf(z.ref, power_above(vtop));
         const float shrink = ref > 0.f ? z.ref / ref : 0.f;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float m = fmaxf(z.m[r], top[r]);
-            const float old = m == -INFINITY ? 1.f : ex2(z.m[r] - m);
-            z.m[r] = m;
-            z.l[r] *= old;
+        for (int t = 0; t < MT; ++t) {
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                z.o[i][2 * r] *= old * shrink;
-                z.o[i][2 * r + 1] *= old * shrink;
+            for (int r = 0; r < 2; ++r) {
+                const float m = fmaxf(z.m[t][r], top[t][r]);
+                const float old = m == -INFINITY ? 1.f : ex2(z.m[t][r] - m);
+                z.m[t][r] = m;
+                z.l[t][r] *= old;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    z.o[t][i][2 * r] *= old * shrink;
+                    z.o[t][i][2 * r + 1] *= old * shrink;
+                }
             }
         }
         z.ref = ref;
     }
     const float unit = z.ref > 0.f ? kWeight / z.ref : 0.f;
-    float wt[2][2][2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) vs[i] *= unit;
     bool light = false;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const float m = z.m[r] == -INFINITY ? 0.f : z.m[r];
-        const bool thin = z.l[r] < kThin;
+    for (int t = 0; t < MT; ++t) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int r = 0; r < 2; ++r) {
+            const float m = z.m[t][r] == -INFINITY ? 0.f : z.m[t][r];
+            const bool thin = z.l[t][r] < kThin;
+            float least = kLeastNormal;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float q = ex2(s[u][2 * r + e] - m);
-                z.l[r] += q;
-                wt[r][u][e] = q * (vs[2 * u + e] * unit);
-                light |= thin && wt[r][u][e] < kLeastNormal && wt[r][u][e] > 0.f;
+            for (int i = 0; i < 8; ++i) {
+                float &y = s[t][i >> 1][2 * r + (i & 1)];
+                y = ex2(y - m);
+                z.l[t][r] += y;
+                y *= vs[i];
+                least = fminf(least, y > 0.f ? y : kLeastNormal);
             }
+            light |= thin && least < kLeastNormal;
         }
     }
     // Weights below fp16's normals lose bits. That shows only where every heavier place holds an exact
     // zero, so only in rows whose weight lies on few places ("thin"); their light weights are added in a
     // pass of their own, scaled up, with the sums scaled along (powers of two: exact).
     light = __any_sync(0xffffffffu, light);
-    uint32_t a[4];
+    uint32_t a[MT][2][4];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) a[2 * u + r] = pack2(wt[r][u][0], wt[r][u][1]);
-    if (light) {
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                a[2 * u + r] = pack2(wt[r][u][0] < kLeastNormal ? 0.f : wt[r][u][0], wt[r][u][1] < kLeastNormal ? 0.f : wt[r][u][1]);
-    }
+            for (int r = 0; r < 2; ++r) {
+                float w0 = s[t][n][2 * r], w1 = s[t][n][2 * r + 1];
+                if (light) w0 = w0 < kLeastNormal ? 0.f : w0, w1 = w1 < kLeastNormal ? 0.f : w1;
+                a[t][n >> 1][2 * (n & 1) + r] = pack2(w0, w1);
+            }
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
-        add_values<FMT, D, MASK>(st, of, a, seen >> 8, z.o);
+        add_values<FMT, D, MT, MASK>(st, of, a, lane, seen.there, z.o);
         if (!light) break;
         const float by = pass ? 1.f / kLift : kLift;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) z.o[i][0] *= by, z.o[i][1] *= by, z.o[i][2] *= by, z.o[i][3] *= by;
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) z.o[t][i][0] *= by, z.o[t][i][1] *= by, z.o[t][i][2] *= by, z.o[t][i][3] *= by;
         if (pass) break;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                a[2 * u + r] = pack2(wt[r][u][0] < kLeastNormal ? wt[r][u][0] * kLift : 0.f,
-                                     wt[r][u][1] < kLeastNormal ? wt[r][u][1] * kLift : 0.f);
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float w0 = s[t][n][2 * r], w1 = s[t][n][2 * r + 1];
+                    a[t][n >> 1][2 * (n & 1) + r] = pack2(w0 < kLeastNormal ? w0 * kLift : 0.f, w1 < kLeastNormal ? w1 * kLift : 0.f);
+                }
     }
 }
 
-// Copies tile `tile` of a job's pages to a stage (one warp). entry: lane i's page of the tile's i-th part.
+// Copies tile `tile` of a job's pages to a stage (the whole warp). Returns the halves of the tile whose page
+// does not exist. entry: the page that the lane copies from; lanes 0 .. 5 copy the (first) page's keys'
+// and values' codes, scales and block scales, lanes 8 .. 13 the second page's when pages hold 16 places.
 template <int FMT, int D>
-__device__ __forceinline__ void fetch(const Attend &p, const Walk &w, int kv, int entry, unsigned char *stage, uint64_t *full,
-                                      uint32_t *bad, int lane) {
+__device__ __forceinline__ uint32_t fetch(const Attend &p, const Walk &w, int tile, int kv, int entry, unsigned char *stage,
+                                          uint64_t *full, int lane) {
     using S = Shape<FMT, D>;
-    const int sub = p.g.page < kTile ? p.g.page : kTile, parts = kTile / sub;
-    const int end = w.n.x + w.n.y;
-    const bool mine = lane < parts && w.tile * kTile + lane * sub < end;
+    const bool halves = p.g.page < kTile;
+    const int part = lane >> 3, kind = (lane >> 1) & 3, which = lane & 1;
+    const int t = tile * kTile + part * 16;
+    const bool mine = (part == 0 || (halves && part == 1)) && kind < (S::kBlocks ? 3 : 2) && t < w.n.x + w.n.y;
     const bool good = mine && entry >= 0 && entry < p.n_pages;
     const uint32_t have = __ballot_sync(0xffffffffu, good), missing = __ballot_sync(0xffffffffu, mine && !good);
-    constexpr int kPer = 2 * (S::kRow + 4 + S::kBlocks);        // bytes of a place
+    const int places = halves ? 16 : kTile;
     if (lane == 0) {
         if (missing) atomicOr(p.flags, QC_FLAG_RANGE);
-        uint32_t m = 0;
-        for (int i = 0; i < parts; ++i)
-            if ((missing >> i) & 1u) m |= ((1u << (sub / 16)) - 1u) << (i * sub / 16);
-        *bad = m;
-        mbar_arrive_expect_tx(full, __popc(have) * sub * kPer);
+        const int parts = (have & 0xffu ? 1 : 0) + (have & 0xff00u ? 1 : 0);
+        mbar_arrive_expect_tx(full, parts * places * (S::kStage / kTile));
     }
     __syncwarp();
-    const unsigned char *head = p.pages + ((int64_t)entry * p.g.heads + kv) * (int64_t)p.g.part;
-    if (p.g.page <= kTile) {
-        if (good) bulk_g2s(stage + lane * sub * kPer, head, sub * kPer, full);
-    } else if (have) {
-        // part of a longer page: its six runs, one lane each
-        const int64_t h0 = __shfl_sync(0xffffffffu, (long long)(head - p.pages), 0);
-        const int t0 = w.tile * kTile & (p.g.page - 1), which = lane & 1, kind = lane >> 1;
-        const unsigned char *src = p.pages + h0;
-        int dst = 0, bytes = 0;
+    if (good) {
+        const unsigned char *src = p.pages + ((int64_t)entry * p.g.heads + kv) * (int64_t)p.g.part;
+        const int at = t & (p.g.page - 1);
+        int dst, bytes;
         if (kind == 0) {
-            src += p.g.codes(which) + t0 * S::kRow;
-            dst = which * kTile * S::kRow;
-            bytes = kTile * S::kRow;
+            src += p.g.codes(which) + at * S::kRow;
+            dst = which * S::kCodes;
+            bytes = S::kRow;
         } else if (kind == 1) {
-            src += p.g.scales(which) + t0 * 4;
-            dst = 2 * kTile * S::kRow + which * kTile * 4;
-            bytes = kTile * 4;
-        } else if (kind == 2 && S::kBlocks) {
-            src += p.g.block_scales(which) + t0 * S::kBlocks;
-            dst = 2 * kTile * (S::kRow + 4) + which * kTile * S::kBlocks;
-            bytes = kTile * S::kBlocks;
+            src += p.g.scales(which) + at * 4;
+            dst = S::kScales + which * kTile * 4;
+            bytes = 4;
+        } else {
+            src += p.g.block_scales(which) + at * S::kBlocks;
+            dst = S::kBlockScales + which * kTile * S::kBlocks;
+            bytes = S::kBlocks;
         }
-        if (bytes) bulk_g2s(stage + dst, src, bytes, full);
+        bulk_g2s(stage + dst + part * 16 * bytes, src, places * bytes, full);
     }
+    const uint32_t bad = (missing & 0xffu ? 1u : 0u) | (missing & 0xff00u ? 2u : 0u);
+    return !halves && bad ? 3u : bad;
 }
 
 template <typename T>
@@ -430,271 +532,204 @@ __device__ __forceinline__ float2 two<__nv_bfloat16>(const __nv_bfloat16 *p) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
 }
 
-// The query rows g and g + 8 of a warp as fragments; up[r]: what a row's scores are multiplied by beside
-// the keys' scales.
-template <typename T, int FMT, int D>
-__device__ __forceinline__ void load_queries(const Attend &p, const Walk &w, int kv, int r0, int R, int g, int c,
-                                             uint32_t (&qa)[D / 16][4], float (&up)[2]) {
+// The query rows as fragments; up: what a row's scores are multiplied by beside the keys' scales.
+template <typename T, int FMT, int D, int MT>
+__device__ __forceinline__ void load_queries(const Attend &p, const Walk &w, int kv, int r0, int R, int lane, Queries<D, MT> &qf,
+                                             uint4 *qs, float (&up)[MT][2]) {
+    const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = r0 + g + 8 * r;
-        const bool there = row < R;
-        const int node = there ? row / p.group : 0, h = there ? row % p.group : 0;
-        const T *q = static_cast<const T *>(p.q) + w.b * p.q_seq + node * p.q_node + (kv * p.group + h) * p.q_head + c * (D / 4);
-        float2 v[D / 8];
+    for (int t = 0; t < MT; ++t) {
+        uint32_t a[2][D / 8];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) v[i] = there ? two(q + 2 * i) : make_float2(0.f, 0.f);
-        float down = 1.f;
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            float top = 0.f;
+        for (int r = 0; r < 2; ++r) {
+            const int row = r0 + 16 * t + g + 8 * r;
+            const bool there = row < R;
+            const int node = there ? row / p.group : 0, h = there ? row % p.group : 0;
+            const T *q = static_cast<const T *>(p.q) + w.b * p.q_seq + node * p.q_node + (kv * p.group + h) * p.q_head + c * (D / 4);
+            float2 v[D / 8];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
-            top = quad_max(top);
-            // largest magnitude to [2^13, 2^14)
-            const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
-            const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-            down = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+            for (int i = 0; i < D / 8; ++i) v[i] = there ? two(q + 2 * i) : make_float2(0.f, 0.f);
+            float down = 1.f;
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                float top = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) v[i].x *= f, v[i].y *= f;
-        }
-        up[r] = p.scale * kLog2e * down;
+                for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+                top = quad_max(top);
+                // largest magnitude to [2^13, 2^14)
+                const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+                const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+                down = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const __half2 x = __floats2half2_rn(v[2 * i + e].x, v[2 * i + e].y);
-                qa[i][2 * e + r] = *reinterpret_cast<const uint32_t *>(&x);
+                for (int i = 0; i < D / 8; ++i) v[i].x *= f, v[i].y *= f;
             }
+            up[t][r] = p.scale * kLog2e * down;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) a[r][i] = pack2(v[i].x, v[i].y);
         }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) qf.put(qs, lane, t, i, a[0][2 * i], a[1][2 * i], a[0][2 * i + 1], a[1][2 * i + 1]);
     }
 }
 
-// What the lane's eight scores of a slice that begins at place t0 see.
-template <int FMT, int D>
-__device__ __forceinline__ uint32_t seen_bits(const Attend &p, const Walk &w, int t0, uint32_t bad, int r0, int R, int g, int c) {
-    if (bad) return 0;
-    uint32_t bits = 0;
+template <int FMT, int D, int MT>
+__device__ __forceinline__ Seen<MT> look(const Attend &p, const Walk &w, int t0, uint32_t bad, int r0, int R, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    Seen<MT> seen;
+    seen.there = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (t0 + Shape<FMT, D>::place(i >> 1, 2 * c + (i & 1)) < w.n.x + w.n.y) bits |= 256u << i;
+    for (int i = 0; i < 8; ++i) {
+        const int t = t0 + 16 * (i >> 2) + Shape<FMT, D>::place((i >> 1) & 1, 2 * c + (i & 1));
+        if (t < w.n.x + w.n.y && !((bad >> (i >> 2)) & 1u)) seen.there |= 1u << i;
+    }
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = r0 + g + 8 * r, node = row / p.group;
-        if (row >= R || node >= w.n.y) continue;
-        const uint32_t *tree = p.tree ? p.tree + ((int64_t)w.b * p.n_nodes + node) * p.words : nullptr;
+    for (int m = 0; m < MT; ++m) {
+        seen.row[m] = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int j = t0 + Shape<FMT, D>::place(i >> 1, 2 * c + (i & 1)) - w.n.x;
-            bool sees = j < 0;
-            if (j >= 0 && j < w.n.y) sees = tree ? (__ldg(tree + (j >> 5)) >> (j & 31)) & 1u : j <= node;
-            if (sees) bits |= 1u << (4 * r + i);
+        for (int r = 0; r < 2; ++r) {
+            const int row = r0 + 16 * m + g + 8 * r, node = row / p.group;
+            if (row >= R || node >= w.n.y) continue;
+            const uint32_t *tree = p.tree ? p.tree + ((int64_t)w.b * p.n_nodes + node) * p.words : nullptr;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = t0 + 16 * (i >> 2) + Shape<FMT, D>::place((i >> 1) & 1, 2 * c + (i & 1)) - w.n.x;
+                bool sees = j < 0;
+                if (j >= 0 && j < w.n.y) sees = tree ? (__ldg(tree + (j >> 5)) >> (j & 31)) & 1u : j <= node;
+                if (sees) seen.row[m] |= 1u << (8 * r + i);
+            }
+            seen.row[m] &= ~(0xffu << (8 * r)) | seen.there << (8 * r);
         }
     }
-    return bits;
+    return seen;
 }
 
-template <typename T, int FMT, int D, int RW>
-__global__ void __launch_bounds__(32 * (kSlices * RW + 1), RW == 1 ? 2 : 1)
-    attend_rows(const Attend p, const Parts parts, const Plan plan) {
+template <typename T, int FMT, int D, int MT>
+__global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const Parts parts, const Plan plan) {
     using S = Shape<FMT, D>;
-    constexpr int kWarps = kSlices * RW;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Shared sh;
-    __shared__ float2 stat[kWarps][kRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ uint64_t full[8];
+    const int lane = threadIdx.x;
     const int R = p.n_nodes * p.group, jobs = p.g.heads * plan.row_tiles;
-    unsigned char *ring = smem;
-    float *sum = reinterpret_cast<float *>(smem + plan.stages * S::kStage);     // [RW][D / 2][32]: joined values
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + plan.stages * S::kStage);
+    if (lane == 0) {
+        for (int i = 0; i < plan.stages; ++i) mbar_init(&full[i], 1);
+        fence_barrier_init();
+    }
+    Offsets<FMT, D> of;
+    of.set(lane >> 2, lane & 3, p.g.page < kTile);
+    __syncwarp();
 
     griddep_wait();
-    if (warp == kWarps) {
-        const int64_t total = all_tiles(p, kTile, lane) * jobs, per = run_length(total, gridDim.x);
-        const int64_t at = per * blockIdx.x, left = at < total ? (total - at < per ? total - at : per) : 0;
-        const Walk w = find(p, at, left, jobs, kTile, lane);
-        if (blockIdx.x == 0) write_before(p, parts.before, jobs, kTile, lane);
-        if (lane == 0) {
-            sh.start = w;
-            sh.fail = 0;
-            for (int i = 0; i < plan.stages; ++i) {
-                mbar_init(&sh.full[i], 1);
-                mbar_init(&sh.empty[i], kWarps);
-            }
-            fence_barrier_init();
-        }
-    }
-    __syncthreads();
-    Walk w = sh.start;
-    int stage = 0;
+    const int64_t total = all_tiles(p, kTile, lane) * jobs, per = run_length(total, gridDim.x), at = per * blockIdx.x;
+    if (blockIdx.x == 0) write_before(p, parts.before, jobs, kTile, lane);
+    Walk w = find(p, at, at < total ? (total - at < per ? total - at : per) : 0, jobs, kTile, lane);
+    int stage = 0, segment = 0;
     uint32_t phase = 0;
-
-    if (warp == kWarps) {
-        // ---- producer
-        const int sub_shift = p.g.shift < 6 ? p.g.shift : 6, parts_of = kTile >> sub_shift;
-        int used = 0;
-        bool ok = true;
-        while (w.left > 0 && ok) {
-            const int kv = w.job / plan.row_tiles;
-            const int32_t *row = p.table + w.b * p.table_stride;
-            const int end = w.n.x + w.n.y;
-            auto entry_of = [&](int tile) {
-                const int t = tile * kTile + (lane << sub_shift);
-                return lane < parts_of && tile < w.tiles && t < end ? __ldg(row + (t >> p.g.shift)) : -1;
-            };
-            int entry = entry_of(w.tile);
-            for (; w.tile < w.tiles && w.left > 0; ++w.tile, --w.left) {
-                const int next = entry_of(w.tile + 1);
-                if (used >= plan.stages) {
-                    // the ring's earlier content must have been read
-                    ok = mbar_wait(&sh.empty[stage], phase ^ 1u);
-                    ok = __all_sync(0xffffffffu, ok) && *(volatile uint32_t *)&sh.fail == 0;
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                }
-                fetch<FMT, D>(p, w, kv, entry, ring + stage * S::kStage, &sh.full[stage], &sh.bad[stage], lane);
-                entry = next;
-                ++used;
-                if (++stage == plan.stages) stage = 0, phase ^= 1u;
+    bool ok = true;
+    while (w.left > 0 && ok) {
+        const int kv = w.job / plan.row_tiles, r0 = w.job % plan.row_tiles * (16 * MT);
+        const int from = w.tile, end = (int)(w.left < w.tiles - from ? from + w.left : w.tiles);
+        const int32_t *row = p.table + w.b * p.table_stride;
+        auto entry_of = [&](int tile) {
+            const int t = tile * kTile + (lane >> 3) * 16;
+            return lane < 16 && tile < end && t < w.n.x + w.n.y ? __ldg(row + (t >> p.g.shift)) : -1;
+        };
+        // the first tiles, then the queries while they travel
+        uint32_t bad = 0;       // two bits per stage
+        int ahead = from, ahead_stage = stage;
+        int entry = entry_of(ahead);
+        auto send = [&]() {
+            const int next = entry_of(ahead + 1);
+            const uint32_t b = fetch<FMT, D>(p, w, ahead, kv, entry, smem + ahead_stage * S::kStage, &full[ahead_stage], lane);
+            bad = (bad & ~(3u << (2 * ahead_stage))) | b << (2 * ahead_stage);
+            entry = next;
+            ++ahead;
+            if (++ahead_stage == plan.stages) ahead_stage = 0;
+        };
+        for (int i = 0; i < plan.stages && ahead < end; ++i) send();
+        Queries<D, MT> q;
+        float up[MT][2];
+        load_queries<T, FMT, D, MT>(p, w, kv, r0, R, lane, q, qs, up);
+        __syncwarp();
+        State<D, MT> z;
+        z.clear();
+        int tile = from;
+        for (; tile < end; ++tile) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase));
+            if (!ok) break;
+            const unsigned char *st = smem + stage * S::kStage;
+            const int t0 = tile * kTile;
+            const uint32_t b = (bad >> (2 * stage)) & 3u;
+            if (t0 + kTile <= w.n.x && !b) {
+                add_tile<FMT, D, MT, false>(st, of, q, qs, up, Seen<MT>{}, lane, z);
+            } else {
+                add_tile<FMT, D, MT, true>(st, of, q, qs, up, look<FMT, D, MT>(p, w, t0, b, r0, R, lane), lane, z);
             }
-            if (ok) next_job(p, w, jobs, kTile);
+            __syncwarp();
+            if (++stage == plan.stages) stage = 0, phase ^= 1u;
+            if (ahead < end) send();
         }
         if (!ok) {
             // let the copies under way land before the CTA's shared memory goes
-            if (lane == 0) atomicOr(p.flags, QC_FLAG_TIMEOUT), atomicExch(&sh.fail, 1u);
-            for (int i = 0; i < plan.stages && i < used; ++i) {
-                if (stage == 0) phase ^= 1u;
-                stage = (stage ? stage : plan.stages) - 1;
-                mbar_wait(&sh.full[stage], phase);
+            if (lane == 0) atomicOr(p.flags, QC_FLAG_TIMEOUT);
+            for (; tile < ahead; ++tile) {
+                mbar_wait(&full[stage], phase);
+                if (++stage == plan.stages) stage = 0, phase ^= 1u;
             }
         }
-        griddep_launch_dependents();
-        return;
-    }
-
-    // ---- consumers
-    const int g = lane >> 2, c = lane & 3, slice_of = warp & (kSlices - 1), rw = warp / kSlices;
-    Offsets<FMT, D> of;
-    of.set(slice_of, p.g.page, g, c);
-    bool ok = true;
-    int segment = 0;
-    while (w.left > 0) {
-        const int kv = w.job / plan.row_tiles, r0 = (w.job % plan.row_tiles * RW + rw) * kRows;
-        const bool whole_before = w.tile == 0;
-        uint32_t qa[D / 16][4];
-        float up[2];
-        load_queries<T, FMT, D>(p, w, kv, r0, R, g, c, qa, up);
-        State<D> z;
-        z.clear();
-        for (; w.tile < w.tiles && w.left > 0; ++w.tile, --w.left) {
-            if (ok && !mbar_wait(&sh.full[stage], phase)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const unsigned char *st = ring + stage * S::kStage;
-            const uint32_t bad = sh.bad[stage];
-            const int t0 = w.tile * kTile + slice_of * 16;
-            if (t0 + 16 <= w.n.x && !bad) {
-                slice<FMT, D, false>(st, of, qa, up, 0xfffu, z);
-            } else if (t0 < w.n.x + w.n.y) {
-                const uint32_t seen = seen_bits<FMT, D>(p, w, t0, (bad >> slice_of) & 1u, r0, R, g, c);
-                slice<FMT, D, true>(st, of, qa, up, seen, z);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty[stage]);
-            if (++stage == plan.stages) stage = 0, phase ^= 1u;
-        }
-        if (!ok) {
-            if (lane == 0) atomicOr(p.flags, QC_FLAG_TIMEOUT), atomicExch(&sh.fail, 1u);
-        }
-        // join the slices' warps: sums of l over the quad, then maxima and values over the warps in order
+        const bool whole = from == 0 && end == w.tiles;
+        // part 2 c: the job that the CTA's run begins with; 2 c + 1: the one it ends with
+        const int64_t part = 2 * (int64_t)blockIdx.x + (segment ? 1 : 0);
+        const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            z.l[r] += __shfl_xor_sync(0xffffffffu, z.l[r], 1);
-            z.l[r] += __shfl_xor_sync(0xffffffffu, z.l[r], 2);
-            if (c == 0) stat[warp][g + 8 * r] = make_float2(z.m[r], z.l[r]);
-        }
-        ok = named_sync_and(1, 32 * kWarps, ok);        // one that gave up takes the others with it
-        float m[2], l[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            m[r] = -INFINITY;
-            l[r] = 0.f;
-#pragma unroll
-            for (int i = 0; i < kSlices; ++i) m[r] = fmaxf(m[r], stat[rw * kSlices + i][g + 8 * r].x);
-#pragma unroll
-            for (int i = 0; i < kSlices; ++i) {
-                const float2 x = stat[rw * kSlices + i][g + 8 * r];
-                if (x.x != -INFINITY) l[r] += x.y * ex2(x.x - m[r]);
-            }
-            const float f = z.m[r] == -INFINITY ? 0.f : ex2(z.m[r] - m[r]) * (z.ref * (1.f / kWeight));
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) z.o[i][2 * r] *= f, z.o[i][2 * r + 1] *= f;
-        }
-        float4 *mine = reinterpret_cast<float4 *>(sum + rw * (D / 2) * 32);
-        for (int turn = 0; turn < kSlices - 1; ++turn) {
-            if (slice_of == turn) {
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    float4 x = make_float4(z.o[i][0], z.o[i][1], z.o[i][2], z.o[i][3]);
-                    if (turn) {
-                        const float4 y = mine[i * 32 + lane];
-                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                    }
-                    mine[i * 32 + lane] = x;
-                }
-            }
-            named_sync(1, 32 * kWarps);
-        }
-        if (slice_of == kSlices - 1) {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                const float4 y = mine[i * 32 + lane];
-                z.o[i][0] += y.x, z.o[i][1] += y.y, z.o[i][2] += y.z, z.o[i][3] += y.w;
-            }
-            const bool whole = whole_before && w.tile == w.tiles;
-            // part 2 c: the job that the CTA's run begins with; 2 c + 1: the one it ends with
-            const int64_t part = 2 * (int64_t)blockIdx.x + (segment ? 1 : 0);
+        for (int t = 0; t < MT; ++t) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int row = r0 + g + 8 * r;
-                if (row >= R) continue;
+                float l = z.l[t][r];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int at_row = 16 * t + g + 8 * r, rr = r0 + at_row;
+                if (rr >= R) continue;
                 float v[D / 4];
+                const float unit = z.ref * (1.f / kWeight);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) v[i] = z.o[i][2 * r], v[D / 8 + i] = z.o[i][2 * r + 1];
+                for (int i = 0; i < D / 8; ++i) v[i] = z.o[t][i][2 * r] * unit, v[D / 8 + i] = z.o[t][i][2 * r + 1] * unit;
                 if (whole) {
-                    const int node = row / p.group, h = kv * p.group + row % p.group;
-                    const bool there = node < w.n.y && l[r] > 0.f;
-                    const float inv = there ? 1.f / l[r] : 0.f;
+                    const int node = rr / p.group, h = kv * p.group + rr % p.group;
+                    const bool there = node < w.n.y && l > 0.f;
+                    const float inv = there ? 1.f / l : 0.f;
 #pragma unroll
                     for (int i = 0; i < D / 4; ++i) v[i] = there ? v[i] * inv : 0.f;
-                    const int64_t at = ((int64_t)w.b * p.n_nodes + node) * p.n_q_heads + h;
-                    store_row<T, D / 4>(static_cast<T *>(p.out) + at * D + c * (D / 4), v);
-                    if (p.lse && c == 0) p.lse[at] = there ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
+                    const int64_t o = ((int64_t)w.b * p.n_nodes + node) * p.n_q_heads + h;
+                    store_row<T, D / 4>(static_cast<T *>(p.out) + o * D + c * (D / 4), v);
+                    if (p.lse && c == 0) p.lse[o] = there ? (z.m[t][r] + log2f(l)) * kLn2 : -INFINITY;
                 } else {
-                    float4 *to = reinterpret_cast<float4 *>(parts.row(part, rw * kRows + g + 8 * r) + c * (D / 4));
+                    float4 *to = reinterpret_cast<float4 *>(parts.row(part, at_row) + c * (D / 4));
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) to[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    if (c == 0) *parts.stat(part, rw * kRows + g + 8 * r) = make_float2(m[r], l[r]);
+                    if (c == 0) *parts.stat(part, at_row) = make_float2(z.m[t][r], l);
                 }
             }
         }
         ++segment;
-        if (!ok) break;
+        w.left -= end - from;
         next_job(p, w, jobs, kTile);
-        named_sync(1, 32 * kWarps);         // stat and sum are free again
     }
+    griddep_launch_dependents();
 }
 
 template <int FMT, int D>
 Plan plan_rows(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
     using S = Shape<FMT, D>;
     Plan p;
-    // Up to 16 rows: one tile of rows, two CTAs on an SM. More: two row tiles share each stage.
-    p.row_warps = rows <= kRows ? 1 : 2;
-    p.row_tiles = (rows + kRows * p.row_warps - 1) / (kRows * p.row_warps);
-    const int per_sm = p.row_warps == 1 ? 2 : 1, room = 216 * 1024 / per_sm - 1024, joined = p.row_warps * kRows * D * 4;
-    p.stages = (room - joined) / S::kStage;
-    if (p.stages > 12) p.stages = 12;
-    p.smem = p.stages * S::kStage + joined;
-    p.ctas = per_sm * c->num_sms;
+    // Up to 16 rows: one row tile per warp, its queries in registers. More: two, which share the codes'
+    // conversion, their queries in shared memory.
+    p.mt = rows <= 16 ? 1 : 2;
+    p.row_tiles = (rows + 16 * p.mt - 1) / (16 * p.mt);
+    const int queries = p.mt == 1 ? 0 : p.mt * 16 * D * 2;
+    p.stages = (kRoom - queries) / S::kStage;
+    if (p.stages > 4) p.stages = 4;
+    p.smem = p.stages * S::kStage + queries;
+    p.ctas = kPerSm * c->num_sms;
     const int64_t most = n_seq * c->heads * p.row_tiles * ((max_len + n_nodes + kTile - 1) / kTile);
     if (p.ctas > most) p.ctas = (int)most;
     return p;
@@ -703,18 +738,15 @@ Plan plan_rows(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_
 template <int FMT, int D>
 int64_t workspace(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
     const Plan p = plan_rows<FMT, D>(c, rows, n_seq, max_len, n_nodes);
-    return workspace_bytes(n_seq, 2 * (int64_t)p.ctas, p.row_warps * kRows, D);
+    return workspace_bytes(n_seq, 2 * (int64_t)p.ctas, p.mt * 16, D);
 }
 
-template <typename T, int FMT, int D, int RW>
+template <typename T, int FMT, int D, int MT>
 cudaError_t run(const Plan &plan, const Attend &p, int type, cudaStream_t s) {
-    const Parts parts = parts_at(p.workspace, p.n_seq, 2 * (int64_t)plan.ctas, RW * kRows, D);
-    static_assert(sizeof(Shared) < 1024, "static shared memory");
-    cudaError_t e = cudaFuncSetAttribute(attend_rows<T, FMT, D, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize, plan.smem);
-    if (e != cudaSuccess) return e;
+    const Parts parts = parts_at(p.workspace, p.n_seq, 2 * (int64_t)plan.ctas, MT * 16, D);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)plan.ctas);
-    cfg.blockDim = dim3(32 * (kSlices * RW + 1));
+    cfg.blockDim = dim3(32);
     cfg.dynamicSmemBytes = plan.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -722,7 +754,7 @@ cudaError_t run(const Plan &plan, const Attend &p, int type, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_rows<T, FMT, D, RW>, p, parts, plan);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_rows<T, FMT, D, MT>, p, parts, plan);
     if (e != cudaSuccess) return e;
     return launch_join(p, parts, type, plan.row_tiles, kTile, plan.ctas, s);
 }
@@ -730,9 +762,8 @@ cudaError_t run(const Plan &plan, const Attend &p, int type, cudaStream_t s) {
 template <int FMT, int D>
 cudaError_t pick(const qc_ctx *c, int type, const Attend &p, cudaStream_t s) {
     const Plan plan = plan_rows<FMT, D>(c, p.n_nodes * p.group, p.n_seq, p.max_len, p.n_nodes);
-    if (type == QC_F16)
-        return plan.row_warps == 1 ? run<__half, FMT, D, 1>(plan, p, type, s) : run<__half, FMT, D, 2>(plan, p, type, s);
-    return plan.row_warps == 1 ? run<__nv_bfloat16, FMT, D, 1>(plan, p, type, s) : run<__nv_bfloat16, FMT, D, 2>(plan, p, type, s);
+    if (type == QC_F16) return plan.mt == 1 ? run<__half, FMT, D, 1>(plan, p, type, s) : run<__half, FMT, D, 2>(plan, p, type, s);
+    return plan.mt == 1 ? run<__nv_bfloat16, FMT, D, 1>(plan, p, type, s) : run<__nv_bfloat16, FMT, D, 2>(plan, p, type, s);
 }
 
 }  // namespace
