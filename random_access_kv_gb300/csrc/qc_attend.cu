@@ -8,10 +8,21 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// One warp per query row. Rows of jobs within one CTA are done already; the others' parts lie in
-// consecutive CTAs: part 2 c + 1 of the first (part 2 c if the job begins its run), part 2 c of the rest.
+template <int N>
+__device__ __forceinline__ void load_row(const float *p, float (&v)[N]) {
+    if constexpr (N == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = *reinterpret_cast<const float2 *>(p);
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
+// One warp per query row. Rows of jobs within one unit are done already; the others' parts lie in
+// consecutive units: part 2 c + 1 of the first (part 2 c if the job begins its run), part 2 c of the rest.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) join_parts(const Attend p, const Parts parts, int row_tiles, int tile, int ctas) {
+__global__ void __launch_bounds__(kThreads) join_parts(const Attend p, const Parts parts, int row_tiles, int tile, int units) {
     fq::sm100::griddep_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
@@ -28,22 +39,44 @@ __global__ void __launch_bounds__(kThreads) join_parts(const Attend p, const Par
     for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
     if (tiles && r / p.group < n.y) {
         const int64_t before = parts.before[b], total = parts.before[p.n_seq];
-        const int64_t per = run_length(total, ctas);
+        const int64_t per = run_length(total, units);
         const int64_t first = before + (int64_t)(h * row_tiles + rt) * tiles;
         const int64_t c0 = first / per, c1 = (first + tiles - 1) / per;
         if (c0 == c1) return;
         const int64_t p0 = 2 * c0 + (first == c0 * per ? 0 : 1);
-        for (int64_t c = c0; c <= c1; ++c) m = fmaxf(m, parts.stat(c == c0 ? p0 : 2 * c, rr)->x);
-        const float ref = m == -INFINITY ? 0.f : m;
-        for (int64_t c = c0; c <= c1; ++c) {
-            const int64_t at = c == c0 ? p0 : 2 * c;
-            const float2 s = *parts.stat(at, rr);
-            const float w = exp2f(s.x - ref);
-            l = fmaf(s.y, w, l);
-            const float *v = parts.row(at, rr) + lane * (D / 32);
+        // all parts' maxima first, a lane each; then the values, several loads under way
+        for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, parts.stat(c == c0 ? p0 : 2 * c, rr)->x);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) o[i] = fmaf(v[i], w, o[i]);
+        for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        const float ref = m == -INFINITY ? 0.f : m;
+        for (int64_t cb = c0; cb <= c1; cb += 32) {
+            const int n = (int)(c1 - cb + 1 < 32 ? c1 - cb + 1 : 32);
+            float2 st = make_float2(-INFINITY, 0.f);
+            if (lane < n) st = *parts.stat(cb + lane == c0 ? p0 : 2 * (cb + lane), rr);
+            const float w = exp2f(st.x - ref);
+            l += st.y * w;                      // this lane's parts
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float v[8][D / 32], wi[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t c = cb + i0 + i;
+                    wi[i] = __shfl_sync(0xffffffffu, w, (i0 + i) & 31);
+                    if (i0 + i < n) {
+                        load_row<D / 32>(parts.row(c == c0 ? p0 : 2 * c, rr) + lane * (D / 32), v[i]);
+                    } else {
+                        wi[i] = 0.f;
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) v[i][j] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) o[j] = fmaf(v[i][j], wi[i], o[j]);
+            }
         }
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
     T *out = static_cast<T *>(p.out) + out_row * D + lane * (D / 32);
@@ -54,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) join_parts(const Attend p, const Par
 }
 
 template <typename T, int D>
-cudaError_t join(const Attend &p, const Parts &parts, int row_tiles, int tile, int ctas, cudaStream_t s) {
+cudaError_t join(const Attend &p, const Parts &parts, int row_tiles, int tile, int units, cudaStream_t s) {
     const int64_t rows = (int64_t)p.n_seq * p.n_nodes * p.n_q_heads;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
@@ -65,17 +98,17 @@ cudaError_t join(const Attend &p, const Parts &parts, int row_tiles, int tile, i
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_parts<T, D>, p, parts, row_tiles, tile, ctas);
+    return cudaLaunchKernelEx(&cfg, join_parts<T, D>, p, parts, row_tiles, tile, units);
 }
 
 }  // namespace
 
-cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int ctas, cudaStream_t s) {
+cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int units, cudaStream_t s) {
     if (type == QC_F16)
-        return p.g.d == 64 ? join<__half, 64>(p, parts, row_tiles, tile, ctas, s)
-                           : join<__half, 128>(p, parts, row_tiles, tile, ctas, s);
-    return p.g.d == 64 ? join<__nv_bfloat16, 64>(p, parts, row_tiles, tile, ctas, s)
-                       : join<__nv_bfloat16, 128>(p, parts, row_tiles, tile, ctas, s);
+        return p.g.d == 64 ? join<__half, 64>(p, parts, row_tiles, tile, units, s)
+                           : join<__half, 128>(p, parts, row_tiles, tile, units, s);
+    return p.g.d == 64 ? join<__nv_bfloat16, 64>(p, parts, row_tiles, tile, units, s)
+                       : join<__nv_bfloat16, 128>(p, parts, row_tiles, tile, units, s);
 }
 
 int64_t attend_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {

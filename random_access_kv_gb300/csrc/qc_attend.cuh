@@ -3,9 +3,9 @@
 //
 // A job is one (sequence, key/value head, tile of query rows); row r of a sequence's head is node r /
 // group, query head r % group of that head. A job's places come in tiles of a kernel's own length. All
-// tiles of all jobs, in order, are dealt to the CTAs in runs of equal length, so that sequences of
-// unlike lengths fill the card evenly; a CTA may end one job and begin the next. A job that lies within
-// one CTA's run is written out by it. Of any other, each CTA leaves its part (running maximum m, sum l,
+// tiles of all jobs, in order, are dealt to the units (warps or CTAs) in runs of equal length, so that sequences of
+// unlike lengths fill the card evenly; a unit may end one job and begin the next. A job that lies within
+// one unit's run is written out by it. Of any other, each unit leaves its part (running maximum m, sum l,
 // and weighted values, all float32) in the workspace, and `join_parts` adds the parts in order.
 #pragma once
 
@@ -40,12 +40,12 @@ __device__ __forceinline__ int64_t all_tiles(const Attend &p, int tile, int lane
     return sum;
 }
 
-// A CTA's place in the order of tiles.
+// A unit's place in the order of tiles.
 struct Walk {
     int b, job, tile;       // sequence, job within it (head * row tiles + row tile), tile within the job
     int tiles;              // tiles of the job
     int2 n;                 // lengths of the sequence
-    int64_t left;           // tiles that the CTA still has, this one included
+    int64_t left;           // tiles that the unit still has, this one included
 };
 
 // Fills `before` (one warp).
@@ -101,7 +101,7 @@ __device__ __forceinline__ Walk find(const Attend &p, int64_t at, int64_t left, 
     }
 }
 
-// The next job's first tile. False at the end of the CTA's run.
+// The next job's first tile. False at the end of the unit's run.
 __device__ __forceinline__ bool next_job(const Attend &p, Walk &w, int jobs, int tile) {
     if (w.left <= 0) return false;
     w.tile = 0;
@@ -116,11 +116,11 @@ __device__ __forceinline__ bool next_job(const Attend &p, Walk &w, int jobs, int
     return false;
 }
 
-// Tiles per CTA, and so the CTA of a tile.
-__device__ __forceinline__ int64_t run_length(int64_t total, int ctas) { return (total + ctas - 1) / ctas; }
+// Tiles per unit, and so the unit of a tile.
+__device__ __forceinline__ int64_t run_length(int64_t total, int units) { return (total + units - 1) / units; }
 
 // The workspace: `before` [n_seq + 1], the tiles of the jobs before each sequence (and of all), and the
-// parts. CTA c's first job (it may have begun in an earlier CTA) is part 2 c, the job
+// parts. unit c's first job (it may have begun in an earlier unit) is part 2 c, the job
 // at the end of its run part 2 c + 1 when that is another one. Per part: values [rows][d], then for
 // all parts (m, l) [rows].
 struct Parts {
@@ -145,8 +145,8 @@ inline Parts parts_at(void *ws, int64_t n_seq, int64_t parts, int rows, int d) {
     return r;
 }
 
-// Joins the parts of every job that lies in several CTAs, and writes the zeros of sequences without tiles.
-cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int ctas, cudaStream_t s);
+// Joins the parts of every job that lies in several units, and writes the zeros of sequences without tiles.
+cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int units, cudaStream_t s);
 
 // The kernels (qc_attend_rows.cu).
 cudaError_t launch_attend_rows(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);

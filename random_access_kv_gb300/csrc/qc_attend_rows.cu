@@ -1,8 +1,8 @@
 // Attention over the quantised cache for few query rows per key/value head (single tokens, chains,
 // small trees).
 //
-// What bounds it: the pages, read once. Every warp is a CTA of its own, eight on an SM, with a run of
-// tiles of 32 places. It copies them from the pages, as they lie, to its ring of shared-memory stages
+// What bounds it: the pages, read once. Each of the eight warps on an SM (two CTAs of four, so that every
+// scheduler has two) has a run of tiles of 32 places of its own. It copies them from the pages, as they lie, to its ring of shared-memory stages
 // with bulk asynchronous copies, two or more tiles ahead, and turns codes into tensor-core fragments in
 // registers. Warps never wait for one another; what one leaves unused of the memory's bandwidth, for
 // instance at the start of a job, the other seven on its SM take.
@@ -10,9 +10,12 @@
 // Products. Codes are exact in fp16, and so are e2m1 codes times their e4m3 block scale (5 bits), so
 // the products q . code are exact and summed in float32; the row's scale multiplies the score
 // afterwards. A bf16 query row is brought into fp16's range by a power of two (8 bits fit 11). For the
-// values, the weight p_t times the row's scale is the operand: w_t = p_t * (s_t / ref) * 2^14, ref a
-// power of two, the running bound of the scales seen. p_t <= 1, so w_t <= 2^14 keeps fp16's 11 bits over
-// 28 binades; `slice` says what becomes of lighter weights.
+// values, the weight p_t times the row's scale is the operand: w_t = p_t * (s_t / ref) * 2^12, ref a
+// power of two, the running bound of the scales seen. A row's reference m moves only when a score passes
+// it by 3 (base 2), to 3 above that score: so p_t <= 2^3 and w_t <= 2^15, the sums are rescaled seldom
+// (a first tile's reference serves until a score is 2^6 times heavier), and the maximum is only reduced
+// over a row's lanes when it is. w_t keeps fp16's 11 bits down to 2^-14; `add_tile` says what becomes of
+// lighter weights.
 //
 // Order of elements. A sum over d may take them in any order as long as both operands do: lane c of a
 // quad takes elements c d / 4 .. of a key, so one 16-byte load feeds four (e2m1: eight) steps. For the
@@ -29,12 +32,15 @@ namespace {
 using namespace fq::sm100;
 
 constexpr int kTile = 32;               // places per stage
-constexpr int kPerSm = 8;               // CTAs (warps) on an SM: 255 registers and 27 KB each
+constexpr int kPerSm = 8, kWarps = 4;   // warps on an SM (255 registers and 27 KB each) and of a CTA
 constexpr int kRoom = 27 * 1024;
-constexpr float kWeight = 16384.f;      // 2^14
+constexpr float kWeight = 4096.f;       // 2^12
+constexpr float kLag = 3.f;             // how far (base 2) a score may pass the row's reference, and how far
+                                        // above the maximum a new reference is put
 constexpr float kLeastNormal = 6.103515625e-05f;    // 2^-14, fp16's
 constexpr float kLift = 16777216.f;     // 2^24
-constexpr float kThin = 2.f;            // about a quarter of a row's sum of weights, the heaviest being 1
+constexpr float kHeavy = 2.44140625e-04f;   // 2^-12
+constexpr int kSettled = 12;            // heavy places that a row must have met
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -45,6 +51,12 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -93,8 +105,8 @@ struct Plan {
     int row_tiles;      // tiles of 16 MT rows per head
     int mt;             // 16-row tiles of a warp (1 or 2)
     int stages;
-    int ctas;
-    int smem;
+    int units;          // warps
+    int smem;           // of a warp
 };
 
 // One lane's offsets within a stage. Rows of 128 and 64 bytes: the other offsets are these plus
@@ -334,11 +346,15 @@ __device__ __forceinline__ void add_values(const unsigned char *st, const Offset
 // The softmax state of a warp's rows: a thread holds rows g and g + 8 of each row tile.
 template <int D, int MT>
 struct State {
-    float m[MT][2], l[MT][2];   // maximum (base-2 units), this thread's share of the sum
+    float m[MT][2], l[MT][2];   // reference (base-2 units), this thread's share of the sum
     float ref;                  // power of two, bound of the values' scales; 0: none yet
+    int heavy;                  // places of weight kHeavy or more that each row met, 8 bits per row, at most 127
+    bool settled;               // kSettled or more for every row of the warp
     float o[MT][D / 8][4];
     __device__ __forceinline__ void clear() {
         ref = 0.f;
+        heavy = 0;
+        settled = false;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             m[t][0] = m[t][1] = -INFINITY;
@@ -369,7 +385,7 @@ struct Seen {
 
 template <int FMT, int D, int MT, bool MASK>
 __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<FMT, D> &of, const Queries<D, MT> &q, const uint4 *qs,
-                                         const float (&up)[MT][2], const Seen<MT> &seen, int lane, State<D, MT> &z) {
+                                         float up, const float (&down)[MT][2], const Seen<MT> &seen, int lane, State<D, MT> &z) {
     using S = Shape<FMT, D>;
     float s[MT][4][4];
     scores<FMT, D, MT>(st, of, q, qs, lane, s);
@@ -378,35 +394,37 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
     load_scales<S::kRow>(st + S::kScales + 4 * kTile, lane & 3, vs);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        ks[i] *= up;
         if (MASK && !((seen.there >> i) & 1u)) vs[i] = 0.f;
         vtop = fmaxf(vtop, vs[i]);
     }
-    vtop = quad_max(vtop);
     bool grows = vtop > z.ref;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            float x = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float &y = s[t][i >> 1][2 * r + (i & 1)];
-                y *= ks[i] * up[t][r];
+                y *= ks[i];
                 if (MASK && !((seen.row[t] >> (8 * r + i)) & 1u)) y = -INFINITY;
-                x = fmaxf(x, y);
             }
-            top[t][r] = quad_max(x);
-            grows |= top[t][r] > z.m[t][r];
+            float x = fmax3(s[t][0][2 * r], s[t][0][2 * r + 1], s[t][1][2 * r]);
+            x = fmax3(x, s[t][1][2 * r + 1], s[t][2][2 * r]);
+            x = fmax3(x, s[t][2][2 * r + 1], s[t][3][2 * r]);
+            top[t][r] = fmaxf(x, s[t][3][2 * r + 1]) * down[t][r];
+            grows |= top[t][r] > z.m[t][r] + kLag;
         }
     }
     if (__any_sync(0xffffffffu, grows)) {
-        const float ref = fmaxf(z.ref, power_above(vtop));
+        const float ref = fmaxf(z.ref, power_above(quad_max(vtop)));
         const float shrink = ref > 0.f ? z.ref / ref : 0.f;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float m = fmaxf(z.m[t][r], top[t][r]);
+                const float x = quad_max(top[t][r]);
+                const float m = x > z.m[t][r] + kLag ? x + kLag : z.m[t][r];
                 const float old = m == -INFINITY ? 1.f : ex2(z.m[t][r] - m);
                 z.m[t][r] = m;
                 z.l[t][r] *= old;
@@ -418,33 +436,57 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
             }
         }
         z.ref = ref;
+        z.heavy = 0;
+        z.settled = false;
     }
     const float unit = z.ref > 0.f ? kWeight / z.ref : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) vs[i] *= unit;
-    bool light = false;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const float m = z.m[t][r] == -INFINITY ? 0.f : z.m[t][r];
-            const bool thin = z.l[t][r] < kThin;
-            float least = kLeastNormal;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float &y = s[t][i >> 1][2 * r + (i & 1)];
-                y = ex2(y - m);
+                y = ex2(fmaf(y, down[t][r], -m));
                 z.l[t][r] += y;
                 y *= vs[i];
-                least = fminf(least, y > 0.f ? y : kLeastNormal);
             }
-            light |= thin && least < kLeastNormal;
         }
     }
-    // Weights below fp16's normals lose bits. That shows only where every heavier place holds an exact
-    // zero, so only in rows whose weight lies on few places ("thin"); their light weights are added in a
-    // pass of their own, scaled up, with the sums scaled along (powers of two: exact).
-    light = __any_sync(0xffffffffu, light);
+    // Weights below fp16's normals are off by up to 2^-25, which shows only where all heavier places hold
+    // an exact zero. Once a row has met a dozen places of weight 2^-12 or more since its reference last
+    // moved, no element has only zeros in them and the error is below 2^-11 of the sum. Until then, what
+    // the rounding of light weights leaves is added in a pass of its own, scaled up, with the sums scaled
+    // along (powers of two: exact).
+    bool light = false;
+    if (!z.settled) {
+        bool few = false;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float least = kLeastNormal;
+                int n = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float y = s[t][i >> 1][2 * r + (i & 1)];
+                    n += y >= kHeavy;
+                    least = fminf(least, y > 0.f ? y : kLeastNormal);
+                }
+                n += __shfl_xor_sync(0xffffffffu, n, 1);
+                n += __shfl_xor_sync(0xffffffffu, n, 2);
+                n = min(n + ((z.heavy >> (16 * t + 8 * r)) & 0xff), 127);
+                z.heavy = (z.heavy & ~(0xff << (16 * t + 8 * r))) | n << (16 * t + 8 * r);
+                few |= n < kSettled;
+                light |= n < kSettled && least < kLeastNormal;
+            }
+        }
+        light = __any_sync(0xffffffffu, light);
+        z.settled = !__any_sync(0xffffffffu, few);
+    }
     uint32_t a[MT][2][4];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -452,9 +494,7 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
         for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                float w0 = s[t][n][2 * r], w1 = s[t][n][2 * r + 1];
-                if (light) w0 = w0 < kLeastNormal ? 0.f : w0, w1 = w1 < kLeastNormal ? 0.f : w1;
-                a[t][n >> 1][2 * (n & 1) + r] = pack2(w0, w1);
+                a[t][n >> 1][2 * (n & 1) + r] = pack2(s[t][n][2 * r], s[t][n][2 * r + 1]);
             }
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
@@ -473,7 +513,8 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float w0 = s[t][n][2 * r], w1 = s[t][n][2 * r + 1];
-                    a[t][n >> 1][2 * (n & 1) + r] = pack2(w0 < kLeastNormal ? w0 * kLift : 0.f, w1 < kLeastNormal ? w1 * kLift : 0.f);
+                    const float2 had = float2_of(a[t][n >> 1][2 * (n & 1) + r]);
+                    a[t][n >> 1][2 * (n & 1) + r] = pack2(w0 < kLeastNormal ? (w0 - had.x) * kLift : 0.f, w1 < kLeastNormal ? (w1 - had.y) * kLift : 0.f);
                 }
     }
 }
@@ -521,21 +562,10 @@ __device__ __forceinline__ uint32_t fetch(const Attend &p, const Walk &w, int ti
     return !halves && bad ? 3u : bad;
 }
 
-template <typename T>
-__device__ __forceinline__ float2 two(const T *p);
-template <>
-__device__ __forceinline__ float2 two<__half>(const __half *p) {
-    return __half22float2(*reinterpret_cast<const __half2 *>(p));
-}
-template <>
-__device__ __forceinline__ float2 two<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p));
-}
-
-// The query rows as fragments; up: what a row's scores are multiplied by beside the keys' scales.
+// The query rows as fragments; down: the power of two that a row's scores are multiplied by.
 template <typename T, int FMT, int D, int MT>
 __device__ __forceinline__ void load_queries(const Attend &p, const Walk &w, int kv, int r0, int R, int lane, Queries<D, MT> &qf,
-                                             uint4 *qs, float (&up)[MT][2]) {
+                                             uint4 *qs, float (&down)[MT][2]) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -546,70 +576,99 @@ __device__ __forceinline__ void load_queries(const Attend &p, const Walk &w, int
             const bool there = row < R;
             const int node = there ? row / p.group : 0, h = there ? row % p.group : 0;
             const T *q = static_cast<const T *>(p.q) + w.b * p.q_seq + node * p.q_node + (kv * p.group + h) * p.q_head + c * (D / 4);
-            float2 v[D / 8];
+            float v[D / 4];
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) v[i] = there ? two(q + 2 * i) : make_float2(0.f, 0.f);
-            float down = 1.f;
+            for (int i = 0; i < D / 32; ++i) {
+                Eight<T> e;
+                float f[8] = {};
+                if (there) {
+                    e.load(q + 8 * i);
+                    e.get(f);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[8 * i + j] = f[j];
+            }
+            down[t][r] = 1.f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                 float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) top = fmaxf(top, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+                for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(v[i]));
                 top = quad_max(top);
                 // largest magnitude to [2^13, 2^14)
                 const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
                 const float f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-                down = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+                down[t][r] = __uint_as_float((uint32_t)(e - 13 + 127) << 23);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) v[i].x *= f, v[i].y *= f;
+                for (int i = 0; i < D / 4; ++i) v[i] *= f;
             }
-            up[t][r] = p.scale * kLog2e * down;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) a[r][i] = pack2(v[i].x, v[i].y);
+            for (int i = 0; i < D / 8; ++i) a[r][i] = pack2(v[2 * i], v[2 * i + 1]);
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) qf.put(qs, lane, t, i, a[0][2 * i], a[1][2 * i], a[0][2 * i + 1], a[1][2 * i + 1]);
     }
 }
 
+// Which of the 32 places from node j0 on (negative: the prefix) node `node` sees, a bit each.
+__device__ __forceinline__ uint32_t window(const Attend &p, const uint32_t *tree, int node, int nodes, int j0) {
+    if (j0 <= -32) return 0xffffffffu;
+    const int k = j0 >> 5;          // -1: the prefix
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = k + i, last = node - 32 * at;
+        if (tree)
+            w[i] = at < 0 ? 0xffffffffu : at < p.words ? __ldg(tree + at) : 0u;
+        else
+            w[i] = last >= 31 ? 0xffffffffu : last < 0 ? 0u : (2u << last) - 1u;
+    }
+    const uint32_t bits = __funnelshift_r(w[0], w[1], j0 & 31);
+    const int there = nodes - j0;
+    return there >= 32 ? bits : there <= 0 ? 0u : bits & ((1u << there) - 1u);
+}
+
 template <int FMT, int D, int MT>
 __device__ __forceinline__ Seen<MT> look(const Attend &p, const Walk &w, int t0, uint32_t bad, int r0, int R, int lane) {
     const int g = lane >> 2, c = lane & 3;
+    const int exist = w.n.x + w.n.y - t0;
+    const uint32_t good = (exist >= 32 ? 0xffffffffu : (1u << max(exist, 0)) - 1u) & ~((bad & 1u ? 0xffffu : 0u) | (bad & 2u ? 0xffff0000u : 0u));
+    uint32_t win[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = r0 + 16 * m + g + 8 * r, node = row < R ? row / p.group : 0;
+            const uint32_t *tree = p.tree ? p.tree + ((int64_t)w.b * p.n_nodes + node) * p.words : nullptr;
+            win[m][r] = window(p, tree, node, w.n.y, t0 - w.n.x);
+            if (row >= R || node >= w.n.y) win[m][r] = 0;
+        }
+    }
     Seen<MT> seen;
     seen.there = 0;
 #pragma unroll
+    for (int m = 0; m < MT; ++m) seen.row[m] = 0;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int t = t0 + 16 * (i >> 2) + Shape<FMT, D>::place((i >> 1) & 1, 2 * c + (i & 1));
-        if (t < w.n.x + w.n.y && !((bad >> (i >> 2)) & 1u)) seen.there |= 1u << i;
-    }
+        const int at = 16 * (i >> 2) + Shape<FMT, D>::place((i >> 1) & 1, 2 * c + (i & 1));
+        seen.there |= ((good >> at) & 1u) << i;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        seen.row[m] = 0;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = r0 + 16 * m + g + 8 * r, node = row / p.group;
-            if (row >= R || node >= w.n.y) continue;
-            const uint32_t *tree = p.tree ? p.tree + ((int64_t)w.b * p.n_nodes + node) * p.words : nullptr;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = t0 + 16 * (i >> 2) + Shape<FMT, D>::place((i >> 1) & 1, 2 * c + (i & 1)) - w.n.x;
-                bool sees = j < 0;
-                if (j >= 0 && j < w.n.y) sees = tree ? (__ldg(tree + (j >> 5)) >> (j & 31)) & 1u : j <= node;
-                if (sees) seen.row[m] |= 1u << (8 * r + i);
-            }
-            seen.row[m] &= ~(0xffu << (8 * r)) | seen.there << (8 * r);
-        }
+            for (int r = 0; r < 2; ++r) seen.row[m] |= (((win[m][r] & good) >> at) & 1u) << (8 * r + i);
     }
     return seen;
 }
 
 template <typename T, int FMT, int D, int MT>
-__global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const Parts parts, const Plan plan) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSm / kWarps) attend_rows(const Attend p, const Parts parts, const Plan plan) {
     using S = Shape<FMT, D>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t full[8];
-    const int lane = threadIdx.x;
+    __shared__ uint64_t bars[kWarps][4];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, unit = blockIdx.x * kWarps + warp;
     const int R = p.n_nodes * p.group, jobs = p.g.heads * plan.row_tiles;
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + plan.stages * S::kStage);
+    uint64_t *full = bars[warp];
+    unsigned char *ring = smem + warp * plan.smem;
+    uint4 *qs = reinterpret_cast<uint4 *>(ring + plan.stages * S::kStage);
     if (lane == 0) {
         for (int i = 0; i < plan.stages; ++i) mbar_init(&full[i], 1);
         fence_barrier_init();
@@ -619,11 +678,12 @@ __global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const 
     __syncwarp();
 
     griddep_wait();
-    const int64_t total = all_tiles(p, kTile, lane) * jobs, per = run_length(total, gridDim.x), at = per * blockIdx.x;
-    if (blockIdx.x == 0) write_before(p, parts.before, jobs, kTile, lane);
+    const int64_t total = all_tiles(p, kTile, lane) * jobs, per = run_length(total, plan.units), at = per * unit;
+    if (unit == 0) write_before(p, parts.before, jobs, kTile, lane);
     Walk w = find(p, at, at < total ? (total - at < per ? total - at : per) : 0, jobs, kTile, lane);
     int stage = 0, segment = 0;
     uint32_t phase = 0;
+    const float up = p.scale * kLog2e;
     bool ok = true;
     while (w.left > 0 && ok) {
         const int kv = w.job / plan.row_tiles, r0 = w.job % plan.row_tiles * (16 * MT);
@@ -639,7 +699,7 @@ __global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const 
         int entry = entry_of(ahead);
         auto send = [&]() {
             const int next = entry_of(ahead + 1);
-            const uint32_t b = fetch<FMT, D>(p, w, ahead, kv, entry, smem + ahead_stage * S::kStage, &full[ahead_stage], lane);
+            const uint32_t b = fetch<FMT, D>(p, w, ahead, kv, entry, ring + ahead_stage * S::kStage, &full[ahead_stage], lane);
             bad = (bad & ~(3u << (2 * ahead_stage))) | b << (2 * ahead_stage);
             entry = next;
             ++ahead;
@@ -647,8 +707,8 @@ __global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const 
         };
         for (int i = 0; i < plan.stages && ahead < end; ++i) send();
         Queries<D, MT> q;
-        float up[MT][2];
-        load_queries<T, FMT, D, MT>(p, w, kv, r0, R, lane, q, qs, up);
+        float down[MT][2];
+        load_queries<T, FMT, D, MT>(p, w, kv, r0, R, lane, q, qs, down);
         __syncwarp();
         State<D, MT> z;
         z.clear();
@@ -656,13 +716,13 @@ __global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const 
         for (; tile < end; ++tile) {
             ok = __all_sync(0xffffffffu, mbar_wait(&full[stage], phase));
             if (!ok) break;
-            const unsigned char *st = smem + stage * S::kStage;
+            const unsigned char *st = ring + stage * S::kStage;
             const int t0 = tile * kTile;
             const uint32_t b = (bad >> (2 * stage)) & 3u;
             if (t0 + kTile <= w.n.x && !b) {
-                add_tile<FMT, D, MT, false>(st, of, q, qs, up, Seen<MT>{}, lane, z);
+                add_tile<FMT, D, MT, false>(st, of, q, qs, up, down, Seen<MT>{}, lane, z);
             } else {
-                add_tile<FMT, D, MT, true>(st, of, q, qs, up, look<FMT, D, MT>(p, w, t0, b, r0, R, lane), lane, z);
+                add_tile<FMT, D, MT, true>(st, of, q, qs, up, down, look<FMT, D, MT>(p, w, t0, b, r0, R, lane), lane, z);
             }
             __syncwarp();
             if (++stage == plan.stages) stage = 0, phase ^= 1u;
@@ -677,8 +737,8 @@ __global__ void __launch_bounds__(32, kPerSm) attend_rows(const Attend p, const 
             }
         }
         const bool whole = from == 0 && end == w.tiles;
-        // part 2 c: the job that the CTA's run begins with; 2 c + 1: the one it ends with
-        const int64_t part = 2 * (int64_t)blockIdx.x + (segment ? 1 : 0);
+        // part 2 c: the job that the warp's run begins with; 2 c + 1: the one it ends with
+        const int64_t part = 2 * (int64_t)unit + (segment ? 1 : 0);
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -729,34 +789,36 @@ Plan plan_rows(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_
     p.stages = (kRoom - queries) / S::kStage;
     if (p.stages > 4) p.stages = 4;
     p.smem = p.stages * S::kStage + queries;
-    p.ctas = kPerSm * c->num_sms;
+    p.units = kPerSm * c->num_sms;
     const int64_t most = n_seq * c->heads * p.row_tiles * ((max_len + n_nodes + kTile - 1) / kTile);
-    if (p.ctas > most) p.ctas = (int)most;
+    if (p.units > most) p.units = (int)(most + kWarps - 1) / kWarps * kWarps;
     return p;
 }
 
 template <int FMT, int D>
 int64_t workspace(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
     const Plan p = plan_rows<FMT, D>(c, rows, n_seq, max_len, n_nodes);
-    return workspace_bytes(n_seq, 2 * (int64_t)p.ctas, p.mt * 16, D);
+    return workspace_bytes(n_seq, 2 * (int64_t)p.units, p.mt * 16, D);
 }
 
 template <typename T, int FMT, int D, int MT>
 cudaError_t run(const Plan &plan, const Attend &p, int type, cudaStream_t s) {
-    const Parts parts = parts_at(p.workspace, p.n_seq, 2 * (int64_t)plan.ctas, MT * 16, D);
+    const Parts parts = parts_at(p.workspace, p.n_seq, 2 * (int64_t)plan.units, MT * 16, D);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)plan.ctas);
-    cfg.blockDim = dim3(32);
-    cfg.dynamicSmemBytes = plan.smem;
+    cfg.gridDim = dim3((unsigned)(plan.units / kWarps));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = kWarps * plan.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_rows<T, FMT, D, MT>, p, parts, plan);
+    cudaError_t e = cudaFuncSetAttribute(attend_rows<T, FMT, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kRoom);
     if (e != cudaSuccess) return e;
-    return launch_join(p, parts, type, plan.row_tiles, kTile, plan.ctas, s);
+    e = cudaLaunchKernelEx(&cfg, attend_rows<T, FMT, D, MT>, p, parts, plan);
+    if (e != cudaSuccess) return e;
+    return launch_join(p, parts, type, plan.row_tiles, kTile, plan.units, s);
 }
 
 template <int FMT, int D>
