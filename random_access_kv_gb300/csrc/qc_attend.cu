@@ -1,5 +1,6 @@
 // Attention over the quantised cache: choice of the kernel, and the joining of the parts that it leaves.
 #include <math.h>
+#include <stdlib.h>
 
 #include "qc_attend.cuh"
 
@@ -111,12 +112,23 @@ cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_t
                        : join<__nv_bfloat16, 128>(p, parts, row_tiles, tile, units, s);
 }
 
+namespace {
+
+// TODO rule
+bool many_rows(int64_t max_len, int n_nodes, int rows) {
+    if (const char *e = getenv("QC_FORCE")) return e[0] == 't';
+    return rows > 16 && max_len + n_nodes >= 1024;
+}
+
+}  // namespace
+
 int64_t attend_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {
-    return rows_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
+    return many_rows(max_len, n_nodes, n_nodes * (n_q_heads / c->heads)) ? tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len)
+                                                                         : rows_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
 }
 
 cudaError_t launch_attend(const qc_ctx *c, int type, const Attend &p, cudaStream_t s) {
-    return launch_attend_rows(c, type, p, s);
+    return many_rows(p.max_len, p.n_nodes, p.n_nodes * p.group) ? launch_attend_tc(c, type, p, s) : launch_attend_rows(c, type, p, s);
 }
 
 }  // namespace qc
