@@ -331,62 +331,45 @@ class CacheContext(Context):
     def __init__(self, handle: int, fmt: str, d: int, n_heads: int, page_tokens: int, device: int):
         super().__init__(handle)
         self.fmt, self.d, self.n_heads, self.page_tokens, self.device = fmt, d, n_heads, page_tokens, device
-        self._as_parameter_cached = ctypes.c_void_p(handle)
-
-    @property
-    def _as_parameter_(self):
-        return self._as_parameter_cached
-
-    def close(self) -> None:
-        super().close()
-        self._as_parameter_cached = ctypes.c_void_p(0)
 
 
-_qc_types = {}
+# A decoding step calls these once per layer, so that their checks count: each call states what it wants of its
+# tensors in one expression, and only when that fails does `_refuse` look for what to say.
+
+_QC_TYPES, _F32, _I32, _I64, _U8 = {}, None, None, None, None
+_raw_stream = None
 
 
-def _qc_type(t) -> int:
-    """QC_* code of a tensor's element type."""
-    if not _qc_types:
-        import torch
-        _qc_types.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
-    code = _qc_types.get(t.dtype)
-    if code is None:
-        raise TypeError(f"rows are float16, bfloat16 or float32, not {t.dtype}")
-    return code
-
-
-def _want(t, what: str, ctx: CacheContext, dtype=None, shape=None) -> None:
-    """Refuses what the C call could not see: another device, type or shape, an inner stride, too few rows."""
-    if t.device.index != ctx.device or t.device.type != "cuda":
-        raise ValueError(f"{what} is on {t.device}, the context on cuda:{ctx.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what} is {t.dtype}, not {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what} is {tuple(t.shape)}, not {shape}")
-
-
-def _want_flat(t, what: str, ctx: CacheContext, dtype, shape=None) -> None:
-    _want(t, what, ctx, dtype, shape)
-    if not t.is_contiguous():
-        raise ValueError(f"{what} is not contiguous")
-
-
-def _want_heads(t, what: str, ctx: CacheContext, dtype, n: int | None = None, heads: int | None = None) -> None:
-    _want(t, what, ctx, dtype)
-    s = t.shape
-    if len(s) != 3 or s[2] != ctx.d or (n is not None and s[0] != n) or (heads is not None and s[1] != heads):
-        raise ValueError(f"{what} is {tuple(s)}, not [{'n' if n is None else n}, {'heads' if heads is None else heads}, {ctx.d}]")
-    if t.stride(2) != 1:
-        raise ValueError(f"{what}: the elements of a row are not next to each other")
-
-
-def _want_pages(pages, ctx: CacheContext) -> int:
+def _qc_init() -> None:
+    """Element types and the current stream's getter, once torch is there."""
+    global _F32, _I32, _I64, _U8, _raw_stream
     import torch
-    _want_flat(pages, "pages", ctx, torch.uint8)
-    if pages.dim() != 2 or pages.shape[1] != qc_page_bytes(ctx):
-        raise ValueError(f"pages is {tuple(pages.shape)}, not [n_pages, {qc_page_bytes(ctx)}]")
-    return pages.shape[0]
+    _QC_TYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    _F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _is(t, dtype, shape, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _refuse(ctx: CacheContext, **what):
+    """Says what is wrong with the tensors `what`: name -> (tensor, element type or None, shape, contiguous). A shape's
+    None is any size."""
+    for name, (t, dtype, shape, flat) in what.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda" or t.device.index != ctx.device:
+            raise ValueError(f"{name} is on {t.device}, the context on cuda:{ctx.device}")
+        if (t.dtype not in _QC_TYPES) if dtype is None else (t.dtype != dtype):
+            raise TypeError(f"{name} is {t.dtype}, not {dtype or 'float16, bfloat16 or float32'}")
+        if len(shape) != t.dim() or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            raise ValueError(f"{name} is {tuple(t.shape)}, not {shape}")
+        if flat and not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise ValueError(f"{name}: the elements of a row are not next to each other")
+    raise ValueError("the arguments do not go together")
 
 
 def qc_create(fmt: str, d: int, n_heads: int, page_tokens: int, device: int = 0) -> CacheContext:
@@ -395,7 +378,11 @@ def qc_create(fmt: str, d: int, n_heads: int, page_tokens: int, device: int = 0)
         raise ValueError(f"fmt is one of {sorted(QC_FORMATS)}, not {fmt!r}")
     h = _c_void_p()
     _check("qc_create", lib().qc_create(ctypes.byref(h), QC_FORMATS[fmt], int(d), int(n_heads), int(page_tokens), int(device)))
-    return CacheContext(h.value, fmt, int(d), int(n_heads), int(page_tokens), int(device))
+    if _raw_stream is None:
+        _qc_init()
+    ctx = CacheContext(h.value, fmt, int(d), int(n_heads), int(page_tokens), int(device))
+    ctx.page_bytes = qc_page_bytes(ctx)
+    return ctx
 
 
 def qc_page_bytes(ctx: CacheContext) -> int:
@@ -405,60 +392,79 @@ def qc_page_bytes(ctx: CacheContext) -> int:
     return int(b)
 
 
+def _qc_stream(stream, dev: int):
+    return _raw_stream(dev) if stream is None else _stream(stream)
+
+
 def qc_norm_rope(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, rot: int, interleaved: bool, q_out, k_out,
                  stream=None) -> None:
     """q [n, hq, d] and k [n, hk, d] (either may be None), strided; w_q, w_k float32 [d] or None; pos int64
     [n]; table float32 [max_pos, rot]; q_out, k_out like q and k (themselves, too)."""
-    import torch
-    args, n, dtype, max_pos = [], None, None, 0
-    for x, out, w, name in ((q, q_out, w_q, "q"), (k, k_out, w_k, "k")):
+    dev, d = ctx.device, ctx.d
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("neither q nor k")
+    dtype, n = x.dtype, x.shape[0]
+    ok, args = dtype in _QC_TYPES, []
+    for x, out, w in ((q, q_out, w_q), (k, k_out, w_k)):
         if x is None:
             args.append((None, 0, 0, 0, None, None, 0, 0))
             continue
-        dtype = x.dtype if dtype is None else dtype
-        _want_heads(x, name, ctx, dtype, n)
-        n = x.shape[0]
-        _want_heads(out, name + "_out", ctx, dtype, n, x.shape[1])
-        if w is not None:
-            _want_flat(w, "w_" + name, ctx, torch.float32, (ctx.d,))
-        args.append((_ptr(x), x.shape[1], x.stride(0), x.stride(1), _ptr(w), _ptr(out), out.stride(0), out.stride(1)))
-    if n is None:
-        raise ValueError("neither q nor k")
-    if rot:
-        _want_flat(pos, "pos", ctx, torch.int64, (n,))
-        _want_flat(table, "table", ctx, torch.float32, (table.shape[0], rot))
-        max_pos = table.shape[0]
+        shape, s, so = x.shape, x.stride(), out.stride()
+        ok = (ok and x.dtype is dtype and out.dtype is dtype and len(shape) == 3 and shape[0] == n and shape[2] == d and out.shape == shape
+              and s[2] == 1 and so[2] == 1 and x.get_device() == dev and out.get_device() == dev
+              and (w is None or _is(w, _F32, (d,), dev)))
+        if not ok:
+            break
+        args.append((x.data_ptr(), shape[1], s[0], s[1], None if w is None else w.data_ptr(), out.data_ptr(), so[0], so[1]))
+    if not ok or (rot and not (_is(pos, _I64, (n,), dev) and _is(table, _F32, (table.shape[0], rot), dev))):
+        rows = {}
+        for name, x, out, w in (("q", q, q_out, w_q), ("k", k, k_out, w_k)):
+            if x is not None:
+                heads = x.shape[1] if x.dim() > 1 else None
+                rows.update({name: (x, None if name == "q" else dtype, (n, heads, d), False), name + "_out": (out, dtype, (n, heads, d), False),
+                             "w_" + name: (w, _F32, (d,), True)})
+        if rot:
+            rows.update(pos=(pos, _I64, (n,), True), table=(table, _F32, (None, rot), True))
+        _refuse(ctx, **rows)
     a, b = args
-    _check("qc_norm_rope", lib().qc_norm_rope(ctx, _qc_type(q if q is not None else k), n, *a[:5], *b[:5], eps,
-                                              _ptr(pos) if rot else None, _ptr(table) if rot else None, max_pos, rot,
-                                              interleaved, *a[5:], *b[5:], _stream(stream)))
+    rc = lib().qc_norm_rope(ctx.handle, _QC_TYPES[dtype], n, *a[:5], *b[:5], eps, pos.data_ptr() if rot else None,
+                            table.data_ptr() if rot else None, table.shape[0] if rot else 0, rot, interleaved, *a[5:], *b[5:],
+                            _qc_stream(stream, dev))
+    if rc:
+        raise FQError("qc_norm_rope", rc)
 
 
 def qc_write(ctx: CacheContext, k, v, slots, pages, stream=None) -> None:
     """k, v [n, n_heads, d], strided; slots int64 [n]; pages uint8 [n_pages, qc_page_bytes(ctx)]."""
-    import torch
-    n = k.shape[0]
-    _want_heads(k, "k", ctx, k.dtype, n, ctx.n_heads)
-    _want_heads(v, "v", ctx, k.dtype, n, ctx.n_heads)
-    _want_flat(slots, "slots", ctx, torch.int64, (n,))
-    n_pages = _want_pages(pages, ctx)
-    _check("qc_write", lib().qc_write(ctx, _qc_type(k), n, _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
-                                      v.stride(1), _ptr(slots), _ptr(pages), n_pages, _stream(stream)))
+    dev, shape, dtype = ctx.device, k.shape, k.dtype
+    n, n_pages, sk, sv = shape[0], pages.shape[0], k.stride(), v.stride()
+    if not (dtype in _QC_TYPES and v.dtype is dtype and shape == (n, ctx.n_heads, ctx.d) and v.shape == shape and sk[2] == 1 and sv[2] == 1
+            and k.get_device() == dev and v.get_device() == dev and _is(slots, _I64, (n,), dev)
+            and _is(pages, _U8, (n_pages, ctx.page_bytes), dev)):
+        _refuse(ctx, k=(k, None, (n, ctx.n_heads, ctx.d), False), v=(v, dtype, (n, ctx.n_heads, ctx.d), False),
+                slots=(slots, _I64, (n,), True), pages=(pages, _U8, (None, ctx.page_bytes), True))
+    rc = lib().qc_write(ctx.handle, _QC_TYPES[dtype], n, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], slots.data_ptr(),
+                        pages.data_ptr(), n_pages, _qc_stream(stream, dev))
+    if rc:
+        raise FQError("qc_write", rc)
 
 
 def qc_read(ctx: CacheContext, pages, slots, k_out, v_out, stream=None) -> None:
     """slots int64 [n]; k_out, v_out [n, n_heads, d], contiguous, or None."""
-    import torch
-    n, n_pages = slots.shape[0], _want_pages(pages, ctx)
-    _want_flat(slots, "slots", ctx, torch.int64, (n,))
+    dev, n, n_pages = ctx.device, slots.shape[0], pages.shape[0]
     out = k_out if k_out is not None else v_out
     if out is None:
         return
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None:
-            _want_flat(t, name, ctx, out.dtype, (n, ctx.n_heads, ctx.d))
-    _check("qc_read", lib().qc_read(ctx, _qc_type(out), n, _ptr(slots), _ptr(pages), n_pages, _ptr(k_out), _ptr(v_out),
-                                    _stream(stream)))
+    dtype, shape = out.dtype, (n, ctx.n_heads, ctx.d)
+    if not (dtype in _QC_TYPES and (k_out is None or _is(k_out, dtype, shape, dev)) and (v_out is None or _is(v_out, dtype, shape, dev))
+            and _is(slots, _I64, (n,), dev) and _is(pages, _U8, (n_pages, ctx.page_bytes), dev)):
+        _refuse(ctx, slots=(slots, _I64, (n,), True), pages=(pages, _U8, (None, ctx.page_bytes), True),
+                k_out=(k_out, None, shape, True), v_out=(v_out, dtype, shape, True))
+    rc = lib().qc_read(ctx.handle, _QC_TYPES[dtype], n, slots.data_ptr(), pages.data_ptr(), n_pages,
+                       None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), _qc_stream(stream, dev))
+    if rc:
+        raise FQError("qc_read", rc)
 
 
 def qc_attend(ctx: CacheContext, pages, q, table, lens, nodes, tree, scale: float, max_len: int, out, lse, workspace,
@@ -466,30 +472,29 @@ def qc_attend(ctx: CacheContext, pages, q, table, lens, nodes, tree, scale: floa
     """q [n_seq, n_nodes, n_q_heads, d], strided; table int32 [n_seq, >= places / page_tokens]; lens, nodes int32
     [n_seq] (nodes may be None); tree int32 [n_seq, n_nodes, ceil(n_nodes / 32)] or None; out like q,
     contiguous; lse float32 [n_seq, n_nodes, n_q_heads] or None; workspace from alloc_attend_workspace."""
-    import torch
-    if q.dim() != 4 or q.shape[3] != ctx.d or q.stride(3) != 1:
-        raise ValueError(f"q is {tuple(q.shape)}, not [n_seq, n_nodes, n_q_heads, {ctx.d}] with its rows' elements together")
-    n_seq, n_nodes, hq, _ = q.shape
-    n_pages = _want_pages(pages, ctx)
-    _want(q, "q", ctx)
-    _want_flat(out, "out", ctx, q.dtype, (n_seq, n_nodes, hq, ctx.d))
-    _want(table, "table", ctx, torch.int32)
-    if table.dim() != 2 or table.shape[0] != n_seq or (table.stride(1) != 1 and table.shape[1] > 1):
-        raise ValueError(f"table is {tuple(table.shape)}, not [{n_seq}, pages per sequence] with rows of their own")
-    if -(-(max_len + n_nodes) // ctx.page_tokens) > table.shape[1]:
+    dev, d, shape, dtype = ctx.device, ctx.d, q.shape, q.dtype
+    if len(shape) != 4:
+        raise ValueError(f"q is {tuple(shape)}, not [n_seq, n_nodes, n_q_heads, {d}]")
+    n_seq, n_nodes, hq, _ = shape
+    n_pages, sq, st, width = pages.shape[0], q.stride(), table.stride(), table.shape[-1]
+    if not (shape[3] == d and sq[3] == 1 and q.get_device() == dev and dtype in _QC_TYPES and _is(out, dtype, shape, dev)
+            and table.dtype is _I32 and table.shape == (n_seq, width) and (st[1] == 1 or width == 1) and table.get_device() == dev
+            and _is(lens, _I32, (n_seq,), dev) and (nodes is None or _is(nodes, _I32, (n_seq,), dev))
+            and (tree is None or _is(tree, _I32, (n_seq, n_nodes, (n_nodes + 31) // 32), dev))
+            and (lse is None or _is(lse, _F32, (n_seq, n_nodes, hq), dev))
+            and _is(pages, _U8, (n_pages, ctx.page_bytes), dev) and _is(workspace, _U8, workspace.shape, dev)):
+        _refuse(ctx, q=(q, None, (n_seq, n_nodes, hq, d), False), out=(out, dtype, (n_seq, n_nodes, hq, d), True),
+                table=(table, _I32, (n_seq, None), False), lens=(lens, _I32, (n_seq,), True), nodes=(nodes, _I32, (n_seq,), True),
+                tree=(tree, _I32, (n_seq, n_nodes, (n_nodes + 31) // 32), True), lse=(lse, _F32, (n_seq, n_nodes, hq), True),
+                pages=(pages, _U8, (None, ctx.page_bytes), True), workspace=(workspace, _U8, (None,), True))
+    if -(-(max_len + n_nodes) // ctx.page_tokens) > width:       # a row's width, which its stride may exceed
         raise FQError("qc_attend", FQ_EINVAL)
-    _want_flat(lens, "lens", ctx, torch.int32, (n_seq,))
-    if nodes is not None:
-        _want_flat(nodes, "nodes", ctx, torch.int32, (n_seq,))
-    if tree is not None:
-        _want_flat(tree, "tree", ctx, torch.int32, (n_seq, n_nodes, (n_nodes + 31) // 32))
-    if lse is not None:
-        _want_flat(lse, "lse", ctx, torch.float32, (n_seq, n_nodes, hq))
-    _want_flat(workspace, "workspace", ctx, torch.uint8)
-    _check("qc_attend", lib().qc_attend(ctx, _qc_type(q), n_seq, n_nodes, hq, _ptr(q), q.stride(0), q.stride(1), q.stride(2),
-                                        _ptr(table), table.stride(0), _ptr(lens), _ptr(nodes), _ptr(tree), _ptr(pages),
-                                        n_pages, scale, max_len, _ptr(out), _ptr(lse), _ptr(workspace),
-                                        workspace.numel(), _stream(stream)))
+    rc = lib().qc_attend(ctx.handle, _QC_TYPES[dtype], n_seq, n_nodes, hq, q.data_ptr(), sq[0], sq[1], sq[2], table.data_ptr(),
+                         st[0] if n_seq > 1 else max(st[0], width), lens.data_ptr(), None if nodes is None else nodes.data_ptr(),
+                         None if tree is None else tree.data_ptr(), pages.data_ptr(), n_pages, scale, max_len, out.data_ptr(),
+                         None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _qc_stream(stream, dev))
+    if rc:
+        raise FQError("qc_attend", rc)
 
 
 def qc_attend_workspace(ctx: CacheContext, n_seq: int, n_nodes: int, n_q_heads: int, max_len: int) -> int:

@@ -115,20 +115,23 @@ cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_t
 namespace {
 
 // TODO rule
-bool many_rows(int64_t max_len, int n_nodes, int rows) {
-    if (const char *e = getenv("QC_FORCE")) return e[0] == 't';
-    return rows > 16 && max_len + n_nodes >= 1024;
+int many_rows(int64_t max_len, int n_nodes, int rows) {
+    if (const char *e = getenv("QC_FORCE")) return e[0] == 't' ? 2 : e[0] == 'c' ? 1 : 0;
+    return max_len + n_nodes < 1024 ? 0 : rows > 64 ? 2 : 1;
 }
 
 }  // namespace
 
 int64_t attend_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {
-    return many_rows(max_len, n_nodes, n_nodes * (n_q_heads / c->heads)) ? tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len)
-                                                                         : rows_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
+    const int k = many_rows(max_len, n_nodes, n_nodes * (n_q_heads / c->heads));
+    return k == 2   ? tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len)
+           : k == 1 ? cols_workspace(c, n_seq, n_nodes, n_q_heads, max_len)
+                    : rows_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
 }
 
 cudaError_t launch_attend(const qc_ctx *c, int type, const Attend &p, cudaStream_t s) {
-    return many_rows(p.max_len, p.n_nodes, p.n_nodes * p.group) ? launch_attend_tc(c, type, p, s) : launch_attend_rows(c, type, p, s);
+    const int k = many_rows(p.max_len, p.n_nodes, p.n_nodes * p.group);
+    return k == 2 ? launch_attend_tc(c, type, p, s) : k == 1 ? launch_attend_cols(c, type, p, s) : launch_attend_rows(c, type, p, s);
 }
 
 }  // namespace qc

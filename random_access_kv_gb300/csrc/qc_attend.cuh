@@ -9,6 +9,7 @@
 // and weighted values, all float32) in the workspace, and `join_parts` adds the parts in order.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "fq_sm100.cuh"
@@ -145,12 +146,25 @@ inline Parts parts_at(void *ws, int64_t n_seq, int64_t parts, int rows, int d) {
     return r;
 }
 
+// Lets a kernel use `bytes` of shared memory on the current device: asked for once per kernel and device (`done`: a
+// bit per device).
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel *kernel, int bytes, int device, std::atomic<uint64_t> &done) {
+    const uint64_t bit = 1ull << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Joins the parts of every job that lies in several units, and writes the zeros of sequences without tiles.
 cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int units, cudaStream_t s);
 
-// The kernels (qc_attend_rows.cu, qc_attend_tc.cu).
+// The kernels (qc_attend_rows.cu, qc_attend_cols.cu, qc_attend_tc.cu).
 cudaError_t launch_attend_rows(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
 int64_t rows_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len);
+cudaError_t launch_attend_cols(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
+int64_t cols_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len);
 cudaError_t launch_attend_tc(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
 int64_t tc_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len);
 

@@ -65,6 +65,7 @@ struct Shape {
 };
 
 struct Plan {
+    int device;
     int row_tiles;      // tiles of 16 MT rows per head
     int mt;             // 16-row tiles of a warp (1 or 2)
     int stages;
@@ -471,47 +472,37 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
     }
 }
 
-// Copies tile `tile` of a job's pages to a stage (the whole warp). Returns the halves of the tile whose page
-// does not exist. entry: the page that the lane copies from; lanes 0 .. 5 copy the (first) page's keys'
-// and values' codes, scales and block scales, lanes 8 .. 13 the second page's when pages hold 16 places.
+// Copies tile `tile` of a job's pages to a stage (the whole warp): keys' and values' codes, scales and block
+// scales; of two pages when pages hold 16 places. entry: lane i's page of the tile's i-th part. Returns the
+// halves of the tile whose page does not exist.
 template <int FMT, int D>
 __device__ __forceinline__ uint32_t fetch(const Attend &p, const Walk &w, int tile, int kv, int entry, unsigned char *stage,
                                           uint64_t *full, int lane) {
     using S = Shape<FMT, D>;
     const bool halves = p.g.page < kTile;
-    const int part = lane >> 3, kind = (lane >> 1) & 3, which = lane & 1;
-    const int t = tile * kTile + part * 16;
-    const bool mine = (part == 0 || (halves && part == 1)) && kind < (S::kBlocks ? 3 : 2) && t < w.n.x + w.n.y;
+    const int parts = halves ? 2 : 1, places = kTile / parts, at = tile * kTile & (p.g.page - 1);
+    const bool mine = lane < parts && tile * kTile + lane * 16 < w.n.x + w.n.y;
     const bool good = mine && entry >= 0 && entry < p.n_pages;
     const uint32_t have = __ballot_sync(0xffffffffu, good), missing = __ballot_sync(0xffffffffu, mine && !good);
-    const int places = halves ? 16 : kTile;
-    if (lane == 0) {
-        if (missing) atomicOr(p.flags, QC_FLAG_RANGE);
-        const int parts = (have & 0xffu ? 1 : 0) + (have & 0xff00u ? 1 : 0);
-        mbar_arrive_expect_tx(full, parts * places * (S::kStage / kTile));
-    }
-    __syncwarp();
-    if (good) {
-        const unsigned char *src = p.pages + ((int64_t)entry * p.g.heads + kv) * (int64_t)p.g.part;
-        const int at = t & (p.g.page - 1);
-        int dst, bytes;
-        if (kind == 0) {
-            src += p.g.codes(which) + at * S::kRow;
-            dst = which * S::kCodes;
-            bytes = S::kRow;
-        } else if (kind == 1) {
-            src += p.g.scales(which) + at * 4;
-            dst = S::kScales + which * kTile * 4;
-            bytes = 4;
-        } else {
-            src += p.g.block_scales(which) + at * S::kBlocks;
-            dst = S::kBlockScales + which * kTile * S::kBlocks;
-            bytes = S::kBlocks;
+    if (missing && lane == 0) atomicOr(p.flags, QC_FLAG_RANGE);
+    if (elect_one()) mbar_arrive_expect_tx(full, __popc(have) * places * (S::kStage / kTile));
+    for (int i = 0; i < parts; ++i) {
+        const int64_t page = __shfl_sync(0xffffffffu, entry, i);
+        if ((have >> i) & 1u) {
+            const unsigned char *src = p.pages + (page * p.g.heads + kv) * (int64_t)p.g.part;
+            if (elect_one()) {
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+                    bulk_g2s(stage + which * S::kCodes + i * 16 * S::kRow, src + p.g.codes(which) + at * S::kRow, places * S::kRow, full);
+                    bulk_g2s(stage + S::kScales + (which * kTile + i * 16) * 4, src + p.g.scales(which) + at * 4, places * 4, full);
+                    if constexpr (S::kBlocks != 0)
+                        bulk_g2s(stage + S::kBlockScales + (which * kTile + i * 16) * S::kBlocks, src + p.g.block_scales(which) + at * S::kBlocks,
+                                 places * S::kBlocks, full);
+                }
+            }
         }
-        bulk_g2s(stage + dst + part * 16 * bytes, src, places * bytes, full);
     }
-    const uint32_t bad = (missing & 0xffu ? 1u : 0u) | (missing & 0xff00u ? 2u : 0u);
-    return !halves && bad ? 3u : bad;
+    return halves ? missing : missing ? 3u : 0u;
 }
 
 // The query rows as fragments; down: the power of two that a row's scores are multiplied by.
@@ -624,8 +615,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm / kWarps) attend_rows(cons
         const int from = w.tile, end = (int)(w.left < w.tiles - from ? from + w.left : w.tiles);
         const int32_t *row = p.table + w.b * p.table_stride;
         auto entry_of = [&](int tile) {
-            const int t = tile * kTile + (lane >> 3) * 16;
-            return lane < 16 && tile < end && t < w.n.x + w.n.y ? __ldg(row + (t >> p.g.shift)) : -1;
+            const int t = tile * kTile + lane * 16;
+            return lane < 2 && tile < end && t < w.n.x + w.n.y ? __ldg(row + (t >> p.g.shift)) : -1;
         };
         // the first tiles, then the queries while they travel
         uint32_t bad = 0;       // two bits per stage
@@ -715,6 +706,7 @@ template <int FMT, int D>
 Plan plan_rows(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
     using S = Shape<FMT, D>;
     Plan p;
+    p.device = c->device;
     // Up to 16 rows: one row tile per warp, its queries in registers. More: two, which share the codes'
     // conversion, their queries in shared memory.
     p.mt = rows <= 16 ? 1 : 2;
@@ -748,7 +740,8 @@ cudaError_t run(const Plan &plan, const Attend &p, int type, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaFuncSetAttribute(attend_rows<T, FMT, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * kRoom);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(attend_rows<T, FMT, D, MT>, kWarps * kRoom, plan.device, done);
     if (e != cudaSuccess) return e;
     e = cudaLaunchKernelEx(&cfg, attend_rows<T, FMT, D, MT>, p, parts, plan);
     if (e != cudaSuccess) return e;

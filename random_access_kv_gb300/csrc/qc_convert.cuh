@@ -5,6 +5,14 @@
 
 namespace qc {
 
+// One lane of a converged warp. Unlike a test of the lane's number it tells the compiler that what follows is
+// one thread's, so that the tensor cores' operands go to uniform registers without a loop over lanes.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
