@@ -2,10 +2,11 @@
 //
 //   y = x * rsqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos - b sin, b cos + a sin) on the first `rot`.
 //
-// Bound by memory: each element is read once and written once for about eight operations. A row is
-// held by d / 8 lanes, eight consecutive elements (16 bytes of a 16-bit type) each; its mean square is
-// a butterfly over those lanes. A warp keeps its token's cosines and sines in registers and takes
-// several heads of the token with them.
+// Bound by memory: each element is read once and written once for about eight operations. A row is held by d
+// / 8 lanes, two groups of four elements each; its mean square is a butterfly over those lanes. Where the
+// pairs lie half the rotated part apart, a lane's second group holds its first group's partners, so that
+// the rotation takes no exchange. A warp keeps its token's cosines and sines in registers and takes several
+// heads of the token with them, their loads under way together.
 #include "qc_formats.cuh"
 
 namespace qc {
@@ -13,82 +14,59 @@ namespace {
 
 constexpr int kThreads = 128;
 
-// One lane's eight cosines and sines, in the order of its elements (pairs of neighbours: four of each).
-struct Turn {
-    float c[8], s[8];
-};
-
 template <typename T, int D, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) norm_rope(const NormRope p, int q_chunks, int k_chunks) {
+__global__ void __launch_bounds__(kThreads) norm_rope(const NormRope p, int q_chunks) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kHeads = kRows * U;
-    const int lane = threadIdx.x & 31, sub = lane / kLanes, e0 = (lane % kLanes) * 8;
-    const int chunks = q_chunks + k_chunks;
-    const int64_t task = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int64_t token = task / chunks;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, i8 = lane % kLanes;
+    const int64_t token = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (token >= p.n) return;
-    int chunk = (int)(task - token * chunks);
-    const bool is_k = chunk >= q_chunks;
-    if (is_k) chunk -= q_chunks;
-    const Heads &t = is_k ? p.k : p.q;
-    const int h0 = chunk * kHeads + sub;
+    const bool is_k = (int)blockIdx.y >= q_chunks;
+    const Heads t = is_k ? p.k : p.q;
+    const int h0 = ((int)blockIdx.y - (is_k ? q_chunks : 0)) * kHeads + sub;
+    // the lane's groups of four: a pair's two halves, or neighbours
+    const int rot = p.rot, half = rot >> 1;
+    const bool turned = 8 * i8 < rot, apart = !INTER && turned;
+    const int ea = apart ? 4 * i8 : 8 * i8, eb = apart ? half + 4 * i8 : 8 * i8 + 4;
 
-    Eight<T> in[U];
-    const T *x = static_cast<const T *>(t.x) + token * t.token + e0;
+    Four<T> in[U][2];
+    const T *x = static_cast<const T *>(t.x) + token * t.token;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int h = h0 + u * kRows;
-        if (h < t.heads) in[u].load(x + h * t.head);
+        if (h < t.heads) {
+            in[u][0].load(x + h * t.head + ea);
+            in[u][1].load(x + h * t.head + eb);
+        }
     }
-
-    const int rot = p.rot, half = rot >> 1;
     bool in_table = true;
-    Turn turn;
-    const bool turned = e0 < rot;
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (rot) {
         const int64_t pos = __ldg(p.pos + token);
         in_table = pos >= 0 && pos < p.max_pos;
         if (!in_table && lane == 0) atomicOr(p.flags, QC_FLAG_RANGE);
         if (in_table && turned) {
-            const float *row = p.table + pos * rot;
-            if constexpr (INTER) {
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(row + e0 / 2));
-                const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half + e0 / 2));
-                turn.c[0] = c.x, turn.c[1] = c.y, turn.c[2] = c.z, turn.c[3] = c.w;
-                turn.s[0] = s.x, turn.s[1] = s.y, turn.s[2] = s.z, turn.s[3] = s.w;
-            } else {
-                // the second half of the rotated elements adds its partner with the other sign
-                const bool second = e0 >= half;
-                const int i0 = second ? e0 - half : e0;
-#pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    const float4 c = __ldg(reinterpret_cast<const float4 *>(row + i0 + i));
-                    const float4 s = __ldg(reinterpret_cast<const float4 *>(row + half + i0 + i));
-                    const float sign = second ? 1.f : -1.f;
-                    turn.c[i] = c.x, turn.c[i + 1] = c.y, turn.c[i + 2] = c.z, turn.c[i + 3] = c.w;
-                    turn.s[i] = sign * s.x, turn.s[i + 1] = sign * s.y, turn.s[i + 2] = sign * s.z,
-                    turn.s[i + 3] = sign * s.w;
-                }
-            }
+            const float *row = p.table + pos * rot + 4 * i8;
+            c = __ldg(reinterpret_cast<const float4 *>(row));
+            s = __ldg(reinterpret_cast<const float4 *>(row + half));
         }
     }
     float w[8];
     if (t.w) {
-        Eight<float> r;
-        r.load(t.w + e0);
+        Four<float> r;
+        r.load(t.w + ea);
         r.get(w);
+        r.load(t.w + eb);
+        r.get(w + 4);
     }
-    // lane that holds the other halves of this lane's pairs (itself beyond the rotated elements)
-    const int away = half / 8;
-    const int partner = !turned ? lane : e0 >= half ? lane - away : lane + away;
-
-    T *out = static_cast<T *>(t.out) + token * t.out_token + e0;
+    T *out = static_cast<T *>(t.out) + token * t.out_token;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int h = h0 + u * kRows;
         const bool there = h < t.heads;
         float v[8];
         if (there) {
-            in[u].get(v);
+            in[u][0].get(v);
+            in[u][1].get(v + 4);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = 0.f;
@@ -103,29 +81,24 @@ __global__ void __launch_bounds__(kThreads) norm_rope(const NormRope p, int q_ch
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = v[i] * r * w[i];
         }
-        if (rot) {
-            if constexpr (INTER) {
-                if (turned && in_table) {
+        if (turned) {
+            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = v[2 * i], b = v[2 * i + 1];
-                        v[2 * i] = a * turn.c[i] - b * turn.s[i];
-                        v[2 * i + 1] = b * turn.c[i] + a * turn.s[i];
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float other = __shfl_sync(0xffffffffu, v[i], partner);
-                    if (turned && in_table) v[i] = v[i] * turn.c[i] + other * turn.s[i];
-                }
-            }
-            if (!in_table) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            for (int i = 0; i < 4; ++i) {
+                float &a = INTER ? v[2 * i] : v[i], &b = INTER ? v[2 * i + 1] : v[4 + i];
+                const float a0 = a, b0 = b;
+                a = a0 * cs[i] - b0 * sn[i];
+                b = b0 * cs[i] + a0 * sn[i];
             }
         }
-        if (there) Eight<T>::store(out + h * t.out_head, v);
+        if (!in_table) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        }
+        if (there) {
+            Four<T>::store(out + h * t.out_head + ea, v);
+            Four<T>::store(out + h * t.out_head + eb, v + 4);
+        }
     }
 }
 
@@ -133,9 +106,9 @@ template <typename T, int D, bool INTER, int U>
 cudaError_t launch(const NormRope &p, cudaStream_t s) {
     constexpr int kHeads = 32 / (D / 8) * U;
     const int qc = (p.q.heads + kHeads - 1) / kHeads, kc = (p.k.heads + kHeads - 1) / kHeads;
-    const int64_t blocks = (p.n * (qc + kc) + kThreads / 32 - 1) / (kThreads / 32);
+    const int64_t blocks = (p.n + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    norm_rope<T, D, INTER, U><<<(unsigned)blocks, kThreads, 0, s>>>(p, qc, kc);
+    norm_rope<T, D, INTER, U><<<dim3((unsigned)blocks, (unsigned)(qc + kc)), kThreads, 0, s>>>(p, qc);
     return cudaGetLastError();
 }
 
