@@ -36,8 +36,8 @@ constexpr int kTile = 32;               // places per stage
 constexpr int kPerSm = 8, kWarps = 4;   // warps on an SM (255 registers and 27 KB each) and of a CTA
 constexpr int kRoom = 27 * 1024;
 constexpr float kWeight = 4096.f;       // 2^12
-constexpr float kLag = 3.f;             // how far (base 2) a score may pass the row's reference, and how far
-                                        // above the maximum a new reference is put
+constexpr float kLag = 3.f;             // how far (base 2) a score may pass the row's reference
+constexpr float kHead = 3.f;            // how far above the largest score a new reference is put
 constexpr float kLeastNormal = 6.103515625e-05f;    // 2^-14, fp16's
 constexpr float kLift = 16777216.f;     // 2^24
 constexpr float kHeavy = 2.44140625e-04f;   // 2^-12
@@ -377,7 +377,7 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 const float x = quad_max(top[t][r]);
-                const float m = x > z.m[t][r] + kLag ? x + kLag : z.m[t][r];
+                const float m = x > z.m[t][r] + kLag ? x + kHead : z.m[t][r];
                 const float old = m == -INFINITY ? 1.f : ex2(z.m[t][r] - m);
                 z.m[t][r] = m;
                 z.l[t][r] *= old;

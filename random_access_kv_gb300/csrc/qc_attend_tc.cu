@@ -9,8 +9,8 @@
 //                        conflicts;
 //   MMA (1 thread)       S = Q K^T into TMEM, then O += P V with P read from TMEM;
 //   softmax (4 NM warps) a thread per row: scores from TMEM, weights back to TMEM as fp16.
-// With NM = 1 the scores are double-buffered, so that the next product runs under the softmax; with NM = 2
-// the two row tiles take turns.
+// Scores and weights of a tile are two halves of 64 places, a buffer each: while a half's softmax runs, the
+// tensor cores take the other half's weights and make the next tile's scores.
 //
 // What bounds it: few rows, the pages (bytes); 128 rows, the issue slots of conversion and softmax; 256
 // rows and more, tensor cores and issue slots alike.
@@ -29,7 +29,8 @@ namespace {
 
 using namespace fq::sm100;
 
-constexpr float kLag = 3.f;
+constexpr float kLag = 3.f;             // how far (base 2) a score may pass the row's reference
+constexpr float kHead = 3.f;            // how far above the largest score a new reference is put
 constexpr int kTop = 12;                // weights' unit: 2^12 over the scales' bound
 constexpr int kMostRaw = 8;
 
@@ -38,14 +39,14 @@ constexpr int kOperand = kTile * D * 2;     // bytes of one fp16 operand tile
 
 struct Bars {
     RawRing raw;
-    uint64_t k_full, k_free, v_full[2], v_free[2], s_full[2], p_ready[2], o_done[2], q_ready, last;
+    uint64_t k_full, k_free, v_full[2], v_free[2], s_full[4], p_ready[4], o_done[2], job_done, q_ready, last;
 };
 
 struct Small {
     Bars b;
-    alignas(16) float ks[4][kTile], vs[2][kTile];       // scales of a tile's places (keys': times scale * log2 e)
+    alignas(16) float ks[4][kTile], vs[4][kTile];       // scales of a tile's places (keys': times scale * log2 e)
     alignas(16) uint32_t exist[4][4];                   // places that exist
-    alignas(16) float vtop[2][4];                       // largest values' scale of each quarter
+    alignas(16) float vtop[4][4];                       // largest values' scale of each quarter
     Walk start;
     uint32_t tmem;
 };
@@ -78,11 +79,14 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&bar.v_full[i], 4);
                 mbar_init(&bar.v_free[i], 1);
-                mbar_init(&bar.s_full[i], 1);
-                mbar_init(&bar.p_ready[i], 4);
                 mbar_init(&bar.o_done[i], 1);
             }
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&bar.s_full[i], 1);
+                mbar_init(&bar.p_ready[i], 4);
+            }
             mbar_init(&bar.q_ready, kSoft);
+            mbar_init(&bar.job_done, 1);
             mbar_init(&bar.last, 1);
             fence_barrier_init();
         }
@@ -128,18 +132,17 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                     if (!ok) break;
                     const unsigned char *st = raw + stage * I::kBytes;
                     const bool good = tile * kTile + t < end && !((bar.raw.bad[stage] >> (t >> 4)) & 1u);
-                    const float s = good ? *reinterpret_cast<const float *>(st + I::kCodes + 4 * t) : 0.f;
                     if (which == 0) {
-                        sm.ks[it & 3][t] = s * up;
-                        const uint32_t e = __ballot_sync(0xffffffffu, good);
-                        if (lane == 0) sm.exist[it & 3][quarter] = e;
-                    } else {
-                        sm.vs[it & 1][t] = s;
-                        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(s));
-                        if (lane == 0) sm.vtop[it & 1][quarter] = __uint_as_float(m);
+                        // the scales, the values' too: the softmax need not wait for the values
+                        const float *scale = reinterpret_cast<const float *>(st + I::kScales) + t;
+                        const float vs = good ? scale[kTile] : 0.f;
+                        sm.ks[it & 3][t] = good ? scale[0] * up : 0.f;
+                        sm.vs[it & 3][t] = vs;
+                        const uint32_t e = __ballot_sync(0xffffffffu, good), m = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
+                        if (lane == 0) sm.exist[it & 3][quarter] = e, sm.vtop[it & 3][quarter] = __uint_as_float(m);
                     }
                     unsigned char *out = which == 0 ? k_op : v_op + (it & 1) * kOp;
-                    convert_row<FMT, D>(st, st + I::kCodes + 4 * kTile + t * I::kBlocks, t, short_runs, good,
+                    convert_row<FMT, D>(st, st + I::kBlockScales + t * I::kBlocks, t, short_runs, good,
                                         [&](int q, const uint32_t(&h)[4]) { put_piece(out, t, q, h); });
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -153,25 +156,26 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
         }
     } else if (warp == kMma) {
         if (elect_one()) {          // one thread, from here to the end
-            const uint32_t qk = idesc_f16_f32(128, kTile), pv = idesc_f16_f32(128, D) | 1u << 16;      // values: output dimension contiguous
+            const uint32_t qk = idesc_f16_f32(128, 64), pv = idesc_f16_f32(128, D) | 1u << 16;      // values: output dimension contiguous
             const uint32_t qa = smem_addr(q_op), ka = smem_addr(k_op), va = smem_addr(v_op);
-            auto scores = [&](int rt, int buf) {        // S[buf] = Q[rt] K^T
+            auto scores = [&](int rt, int h) {          // S[rt][h] = Q[rt] K[half h]^T
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const uint32_t off = (k >> 2) * (kTile * 128) + (k & 3) * 32;
-                    mma_f16(tmem + buf * 128, sdesc_sw128(qa + rt * kOp + off), sdesc_sw128(ka + off), qk, k > 0);
+                    mma_f16(tmem + (2 * rt + h) * 64, sdesc_sw128(qa + rt * kOp + off), sdesc_sw128(ka + h * 8192 + off), qk, k > 0);
                 }
-                mma_commit(&bar.s_full[buf]);
-                if (rt == NM - 1) mma_commit(&bar.k_free);
+                mma_commit(&bar.s_full[2 * rt + h]);
+                if (rt == NM - 1 && h == 1) mma_commit(&bar.k_free);
             };
-            auto values = [&](int rt, int buf, int vb, bool first) {      // O[rt] (+)= P[buf] V[vb]
+            auto values = [&](int rt, int h, int vb, bool first) {      // O[rt] (+)= P[rt][h] V[vb][half h]
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                    mma_f16_ts(tmem + 256 + rt * 128, tmem + buf * 128 + 8 * k, sdesc_sw128_mn(va + vb * kOp + k * 2048, kTile * 128), pv, !first || k > 0);
+                for (int k = 0; k < 4; ++k)
+                    mma_f16_ts(tmem + 256 + rt * 128, tmem + (2 * rt + h) * 64 + 8 * k,
+                               sdesc_sw128_mn(va + vb * kOp + (4 * h + k) * 2048, kTile * 128), pv, !first || k > 0);
                 mma_commit(&bar.o_done[rt]);
-                if (rt == NM - 1) mma_commit(&bar.v_free[vb]);
+                if (rt == NM - 1 && h == 1) mma_commit(&bar.v_free[vb]);
             };
             auto wait = [&](uint64_t *b, uint32_t parity) { ok = ok && wait_phase(b, parity); };
             int segment = 0;
@@ -179,29 +183,21 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                 wait(&bar.q_ready, segment);
                 wait(&bar.k_full, it);
                 if (!ok) break;
-                for (int rt = 0; rt < NM; ++rt) scores(rt, NM == 1 ? it & 1 : rt);
+                for (int i = 0; i < 2 * NM; ++i) scores(i % NM, i / NM);
                 for (int tile = run.from; ok && tile < run.end; ++tile, ++it) {
-                    const bool more = tile + 1 < run.end, first = tile == run.from;
-                    if constexpr (NM == 1) {
-                        if (more) {
-                            wait(&bar.k_full, it + 1);
-                            if (ok) scores(0, (it + 1) & 1);
-                        }
-                        wait(&bar.p_ready[it & 1], it >> 1);
-                        wait(&bar.v_full[it & 1], it >> 1);
-                        if (ok) values(0, it & 1, it & 1, first);
-                    } else {
-                        for (int rt = 0; ok && rt < NM; ++rt) {
-                            wait(&bar.p_ready[rt], it);
-                            if (rt == 0) wait(&bar.v_full[it & 1], it >> 1);
-                            if (ok) values(rt, rt, it & 1, first);
-                            if (more) {
-                                if (rt == 0) wait(&bar.k_full, it + 1);
-                                if (ok) scores(rt, rt);
-                            }
+                    for (int i = 0; ok && i < 2 * NM; ++i) {
+                        const int rt = i % NM, h = i / NM;
+                        wait(&bar.p_ready[2 * rt + h], it);
+                        if (i == 0) wait(&bar.v_full[it & 1], it >> 1);
+                        if (ok) values(rt, h, it & 1, tile == run.from && h == 0);
+                        if (tile + 1 < run.end) {
+                            if (i == 0) wait(&bar.k_full, it + 1);
+                            if (ok) scores(rt, h);
                         }
                     }
                 }
+                // its own barrier: two of the output's phases may end here, which parity does not tell apart
+                mma_commit(&bar.job_done);
             }
             // products under way end before the operands' shared memory and the TMEM go
             mma_commit(&bar.last);
@@ -232,111 +228,111 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             int e = 0;                          // log2 of the weights' unit
             float2 l = make_float2(0.f, 0.f);
             for (int tile = run.from; ok && tile < run.end; ++tile, ++it) {
-                const int buf = NM == 1 ? it & 1 : rt;
-                ok = warp_wait(&bar.s_full[buf], NM == 1 ? it >> 1 : it);
-                // the values' scales of the tile
-                ok = ok && warp_wait(&bar.v_full[it & 1], it >> 1);
-                if (!ok) break;
-                if (active) {
-                    tc_fence_after();
-                    const float4 vt = *reinterpret_cast<const float4 *>(sm.vtop[it & 1]);
-                    const uint4 ex = *reinterpret_cast<const uint4 *>(sm.exist[it & 3]);
-                    const bool mask = tile * kTile + kTile > w.n.x || (ex.x & ex.y & ex.z & ex.w) != 0xffffffffu;
-                    const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
-                    const uint32_t s_at = tmem + lanes + buf * 128;
-                    uint32_t pw[kTile / 2];
-                    float2 sum;
-                    float top;
-                    // one pass with the reference as it is; a second if a score or a scale has passed it
-                    auto sweep = [&](auto masked) {
-                        constexpr bool kMasked = decltype(masked)::value;
-                        const float mm = (m == -INFINITY ? 0.f : m) - (float)e;
-                        const float2 neg = make_float2(-mm, -mm), dn = make_float2(down, down);
-                        float top1 = -INFINITY;
-                        float2 sum1 = make_float2(0.f, 0.f);
-                        top = -INFINITY;
-                        sum = make_float2(0.f, 0.f);
+                for (int half = 0; half < 2; ++half) {
+                    const int buf = 2 * rt + half, place = tile * kTile + 64 * half;
+                    ok = warp_wait(&bar.s_full[buf], it);
+                    if (!ok) break;
+                    if (active) {
+                        tc_fence_after();
+                        const float4 vt = *reinterpret_cast<const float4 *>(sm.vtop[it & 3]);
+                        const uint2 ex = *reinterpret_cast<const uint2 *>(&sm.exist[it & 3][2 * half]);
+                        const bool mask = place + 64 > w.n.x || (ex.x & ex.y) != 0xffffffffu;
+                        const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
+                        const uint32_t s_at = tmem + lanes + buf * 64;
+                        uint32_t pw[32];
+                        float2 sum;
+                        float top;
+                        // one pass with the reference as it is; a second if a score or a scale has passed it
+                        auto sweep = [&](auto masked) {
+                            constexpr bool kMasked = decltype(masked)::value;
+                            const float mm = (m == -INFINITY ? 0.f : m) - (float)e;
+                            const float2 neg = make_float2(-mm, -mm), dn = make_float2(down, down);
+                            float top1 = -INFINITY;
+                            float2 sum1 = make_float2(0.f, 0.f);
+                            top = -INFINITY;
+                            sum = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t s[32];
-                            tmem_ld32_nowait(s_at + 32 * c, s);
-                            uint32_t sees = 0xffffffffu;
-                            if constexpr (kMasked) {
-                                sees = window(p, tree, node, w.n.y, tile * kTile + 32 * c - w.n.x) & (c == 0 ? ex.x : c == 1 ? ex.y : c == 2 ? ex.z : ex.w);
-                                if (!there || node >= w.n.y) sees = 0;
-                            }
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                const float4 ks = *reinterpret_cast<const float4 *>(&sm.ks[it & 3][32 * c + i]);
-                                const float4 vs = *reinterpret_cast<const float4 *>(&sm.vs[it & 1][32 * c + i]);
-                                float2 a = mul2f(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(ks.x, ks.y));
-                                float2 b = mul2f(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(ks.z, ks.w));
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t s[32];
+                                tmem_ld32_nowait(s_at + 32 * c, s);
+                                uint32_t sees = 0xffffffffu;
                                 if constexpr (kMasked) {
-                                    if (!((sees >> i) & 1u)) a.x = -INFINITY;
-                                    if (!((sees >> (i + 1)) & 1u)) a.y = -INFINITY;
-                                    if (!((sees >> (i + 2)) & 1u)) b.x = -INFINITY;
-                                    if (!((sees >> (i + 3)) & 1u)) b.y = -INFINITY;
+                                    sees = window(p, tree, node, w.n.y, place + 32 * c - w.n.x) & (c == 0 ? ex.x : ex.y);
+                                    if (!there || node >= w.n.y) sees = 0;
                                 }
-                                top = fmax3(top, a.x, a.y);
-                                top1 = fmax3(top1, b.x, b.y);
-                                a = fma2f(a, dn, neg);
-                                b = fma2f(b, dn, neg);
-                                a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
-                                sum = add2f(sum, a);
-                                sum1 = add2f(sum1, b);
-                                a = mul2f(a, make_float2(vs.x, vs.y));
-                                b = mul2f(b, make_float2(vs.z, vs.w));
-                                pw[16 * c + i / 2] = pack2(a.x, a.y);
-                                pw[16 * c + i / 2 + 1] = pack2(b.x, b.y);
-                            }
-                        }
-                        top = fmaxf(top, top1);
-                        sum = add2f(sum, sum1);
-                    };
-                    for (int pass = 0;; ++pass) {
-                        if (mask)
-                            sweep(std::true_type{});
-                        else
-                            sweep(std::false_type{});
-                        if (pass) break;
-                        top *= down;
-                        if (!__any_sync(0xffffffffu, top > m + kLag || vtop > ref)) break;
-                        const float m2 = top > m + kLag ? top + kLag : m;
-                        const float ref2 = fmaxf(ref, fmaxf(power_above(vtop), 3.2311742677852644e-27f));     // at least 2^-88
-                        const int e2 = kTop + 127 - (int)(__float_as_uint(ref2) >> 23);
-                        // sums so far in the new unit
-                        const float by = m == -INFINITY ? 0.f : ex2(m - m2 + (float)(e2 - e));
-                        l.x *= by;
-                        l.y *= by;
-                        if (tile > run.from) {
-                            ok = warp_wait(&bar.o_done[rt], it - 1);
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                const uint32_t at = tmem + lanes + 256 + rt * 128 + 32 * c;
-                                tmem_ld32_nowait(at, o);
+                                const float *kp = &sm.ks[it & 3][64 * half + 32 * c], *vp = &sm.vs[it & 3][64 * half + 32 * c];
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-                                tmem_st32(at, o);
+                                for (int i = 0; i < 32; i += 4) {
+                                    const float4 ks = *reinterpret_cast<const float4 *>(kp + i);
+                                    const float4 vs = *reinterpret_cast<const float4 *>(vp + i);
+                                    float2 a = mul2f(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(ks.x, ks.y));
+                                    float2 b = mul2f(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), make_float2(ks.z, ks.w));
+                                    if constexpr (kMasked) {
+                                        if (!((sees >> i) & 1u)) a.x = -INFINITY;
+                                        if (!((sees >> (i + 1)) & 1u)) a.y = -INFINITY;
+                                        if (!((sees >> (i + 2)) & 1u)) b.x = -INFINITY;
+                                        if (!((sees >> (i + 3)) & 1u)) b.y = -INFINITY;
+                                    }
+                                    top = fmax3(top, a.x, a.y);
+                                    top1 = fmax3(top1, b.x, b.y);
+                                    a = fma2f(a, dn, neg);
+                                    b = fma2f(b, dn, neg);
+                                    a.x = ex2(a.x), a.y = ex2(a.y), b.x = ex2(b.x), b.y = ex2(b.y);
+                                    sum = add2f(sum, a);
+                                    sum1 = add2f(sum1, b);
+                                    a = mul2f(a, make_float2(vs.x, vs.y));
+                                    b = mul2f(b, make_float2(vs.z, vs.w));
+                                    pw[16 * c + i / 2] = pack2(a.x, a.y);
+                                    pw[16 * c + i / 2 + 1] = pack2(b.x, b.y);
+                                }
                             }
+                            top = fmaxf(top, top1);
+                            sum = add2f(sum, sum1);
+                        };
+                        for (int pass = 0;; ++pass) {
+                            if (mask)
+                                sweep(std::true_type{});
+                            else
+                                sweep(std::false_type{});
+                            if (pass) break;
+                            top *= down;
+                            if (!__any_sync(0xffffffffu, top > m + kLag || vtop > ref)) break;
+                            const float m2 = top > m + kLag ? top + kHead : m;
+                            const float ref2 = fmaxf(ref, fmaxf(power_above(vtop), 3.2311742677852644e-27f));     // at least 2^-88
+                            const int e2 = kTop + 127 - (int)(__float_as_uint(ref2) >> 23);
+                            // sums so far in the new unit
+                            const float by = m == -INFINITY ? 0.f : ex2(m - m2 + (float)(e2 - e));
+                            l.x *= by;
+                            l.y *= by;
+                            if (tile > run.from || half) {
+                                ok = warp_wait(&bar.o_done[rt], 2 * it + half - 1);
+                                tc_fence_after();
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t o[32];
+                                    const uint32_t at = tmem + lanes + 256 + rt * 128 + 32 * c;
+                                    tmem_ld32_nowait(at, o);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                                    tmem_st32(at, o);
+                                }
+                            }
+                            m = m2;
+                            ref = ref2;
+                            e = e2;
                         }
-                        m = m2;
-                        ref = ref2;
-                        e = e2;
+                        l = add2f(l, sum);
+                        tmem_st32(s_at, pw);
+                        tmem_wait_st();
+                        tc_fence_before();
                     }
-                    l = add2f(l, sum);
-                    tmem_st32(s_at, pw);
-                    tmem_st32(s_at + 32, pw + 32);
-                    tmem_wait_st();
-                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_ready[buf]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_ready[buf]);
             }
-            if (ok) ok = warp_wait(&bar.o_done[rt], it - 1);
+            if (ok) ok = warp_wait(&bar.job_done, segment);
             if (!ok) break;
             if (active) {
                 tc_fence_after();

@@ -75,42 +75,60 @@ struct Eight<float> {
     }
 };
 
-// Four consecutive elements.
+// Four consecutive elements. once: they are touched a single time, and need not stay in the second-level cache.
 template <typename T>
 struct Four;
 template <>
 struct Four<__half> {
     uint2 r;
-    __device__ __forceinline__ void load(const __half *p) { r = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void load(const __half *p, bool once = false) {
+        r = once ? __ldcs(reinterpret_cast<const uint2 *>(p)) : *reinterpret_cast<const uint2 *>(p);
+    }
     __device__ __forceinline__ void get(float *v) const {
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&r.x)), b = __half22float2(*reinterpret_cast<const __half2 *>(&r.y));
         v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
     }
-    static __device__ __forceinline__ void store(__half *p, const float *v) {
+    static __device__ __forceinline__ void store(__half *p, const float *v, bool once = false) {
         const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
-        *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        const uint2 w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        if (once)
+            __stcs(reinterpret_cast<uint2 *>(p), w);
+        else
+            *reinterpret_cast<uint2 *>(p) = w;
     }
 };
 template <>
 struct Four<__nv_bfloat16> {
     uint2 r;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { r = *reinterpret_cast<const uint2 *>(p); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool once = false) {
+        r = once ? __ldcs(reinterpret_cast<const uint2 *>(p)) : *reinterpret_cast<const uint2 *>(p);
+    }
     __device__ __forceinline__ void get(float *v) const {
         v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xffff0000u);
         v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v) {
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *v, bool once = false) {
         const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        const uint2 w = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+        if (once)
+            __stcs(reinterpret_cast<uint2 *>(p), w);
+        else
+            *reinterpret_cast<uint2 *>(p) = w;
     }
 };
 template <>
 struct Four<float> {
     float4 r;
-    __device__ __forceinline__ void load(const float *p) { r = *reinterpret_cast<const float4 *>(p); }
+    __device__ __forceinline__ void load(const float *p, bool once = false) {
+        r = once ? __ldcs(reinterpret_cast<const float4 *>(p)) : *reinterpret_cast<const float4 *>(p);
+    }
     __device__ __forceinline__ void get(float *v) const { v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w; }
-    static __device__ __forceinline__ void store(float *p, const float *v) {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    static __device__ __forceinline__ void store(float *p, const float *v, bool once = false) {
+        const float4 w = make_float4(v[0], v[1], v[2], v[3]);
+        if (once)
+            __stcs(reinterpret_cast<float4 *>(p), w);
+        else
+            *reinterpret_cast<float4 *>(p) = w;
     }
 };
 

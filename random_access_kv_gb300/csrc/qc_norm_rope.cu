@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope(const NormRope p, int q_ch
     for (int u = 0; u < U; ++u) {
         const int h = h0 + u * kRows;
         if (h < t.heads) {
-            in[u][0].load(x + h * t.head + ea);
-            in[u][1].load(x + h * t.head + eb);
+            in[u][0].load(x + h * t.head + ea, U > 1);
+            in[u][1].load(x + h * t.head + eb, U > 1);
         }
     }
     bool in_table = true;
@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope(const NormRope p, int q_ch
             for (int i = 0; i < 8; ++i) v[i] = 0.f;
         }
         if (there) {
-            Four<T>::store(out + h * t.out_head + ea, v);
-            Four<T>::store(out + h * t.out_head + eb, v + 4);
+            Four<T>::store(out + h * t.out_head + ea, v, U > 1);
+            Four<T>::store(out + h * t.out_head + eb, v + 4, U > 1);
         }
     }
 }

@@ -1,5 +1,5 @@
-// What the two tensor-core attention kernels share: tiles of 128 places, the producer warp that copies them
-// from the pages, the conversion of rows to fp16 operands, and the instructions for them.
+// The parts of the tensor-core attention kernel (qc_attend_tc.cu): tiles of 128 places, the producer warps that
+// copy them from the pages, the conversion of rows to fp16 operands, and the instructions for them.
 #pragma once
 
 #include "qc_convert.cuh"
@@ -12,11 +12,12 @@ constexpr int kTile = 128;              // places
 constexpr int kMostRaw = 8;             // raw stages at most
 
 template <int FMT, int D>
-struct Item {           // a raw stage: keys or values of a tile
+struct Item {           // a raw stage: codes and block scales of a tile's keys or values; with the keys both scales
     static constexpr int kRow = FMT == QC_E2M1 ? D / 2 : D;
     static constexpr int kBlocks = FMT == QC_E2M1 ? D / 16 : 0;
     static constexpr int kCodes = kTile * kRow;
-    static constexpr int kBytes = kTile * (kRow + 4 + kBlocks);     // codes, scales, block scales
+    static constexpr int kScales = kCodes, kBlockScales = kCodes + 8 * kTile;
+    static constexpr int kBytes = kTile * (kRow + 8 + kBlocks);
 };
 
 // A place in a unit's run: what every role steps through alike.
@@ -66,17 +67,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
         "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void put_one(__half *p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void put_one(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
 // Two float32 operations at once.
 __device__ __forceinline__ float2 mul2f(float2 a, float2 b) {
@@ -223,19 +214,9 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t phase) {
         }
     }
 }
-#ifdef QC_ONE
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
-    bool ok = true;
-    if (elect_one()) ok = wait_phase(bar, phase);
-    ok = __all_sync(0xffffffffu, ok);
-    __syncwarp();
-    return ok;
-}
-#else
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase) {
     return __all_sync(0xffffffffu, wait_phase(bar, phase));
 }
-#endif
 
 // Issuing a tile's copies takes one warp longer than a tile may take the SM, so that several warps take turns.
 constexpr int kProducers = 3;
@@ -323,9 +304,9 @@ __device__ __forceinline__ bool produce(const Attend &p, Run &run, int jobs, int
                 ring.bad[k] = ring.bad[v] = bad;
                 ring.issued[k] = 1 + (k_round & 1);
                 ring.issued[v] = 1 + (v_round & 1);
-                const uint32_t bytes = __popc(have) * sub * (I::kBytes / kTile);
-                mbar_arrive_expect_tx(&ring.full[k], bytes);
-                mbar_arrive_expect_tx(&ring.full[v], bytes);
+                const uint32_t places = __popc(have) * sub;
+                mbar_arrive_expect_tx(&ring.full[k], places * (I::kRow + 8 + I::kBlocks));
+                mbar_arrive_expect_tx(&ring.full[v], places * (I::kRow + I::kBlocks));
             }
             for (int i = 0; i < parts; ++i) {
                 const int64_t page = __shfl_sync(0xffffffffu, entry, i);
@@ -334,13 +315,13 @@ __device__ __forceinline__ bool produce(const Attend &p, Run &run, int jobs, int
                     const int first = i << sub_shift;
                     if (elect_one()) {
                         bulk_g2s(kt + first * I::kRow, src + at * I::kRow, sub * I::kRow, &ring.full[k]);
-                        bulk_g2s(kt + I::kCodes + first * 4, src + p.g.scales(0) + at * 4, sub * 4, &ring.full[k]);
+                        bulk_g2s(kt + I::kScales + first * 4, src + p.g.scales(0) + at * 4, sub * 4, &ring.full[k]);
+                        bulk_g2s(kt + I::kScales + (kTile + first) * 4, src + p.g.scales(1) + at * 4, sub * 4, &ring.full[k]);
                         bulk_g2s(vt + first * I::kRow, src + p.g.codes(1) + at * I::kRow, sub * I::kRow, &ring.full[v]);
-                        bulk_g2s(vt + I::kCodes + first * 4, src + p.g.scales(1) + at * 4, sub * 4, &ring.full[v]);
                         if constexpr (I::kBlocks != 0) {
-                            bulk_g2s(kt + I::kCodes + 4 * kTile + first * I::kBlocks, src + p.g.block_scales(0) + at * I::kBlocks,
+                            bulk_g2s(kt + I::kBlockScales + first * I::kBlocks, src + p.g.block_scales(0) + at * I::kBlocks,
                                      sub * I::kBlocks, &ring.full[k]);
-                            bulk_g2s(vt + I::kCodes + 4 * kTile + first * I::kBlocks, src + p.g.block_scales(1) + at * I::kBlocks,
+                            bulk_g2s(vt + I::kBlockScales + first * I::kBlocks, src + p.g.block_scales(1) + at * I::kBlocks,
                                      sub * I::kBlocks, &ring.full[v]);
                         }
                     }
