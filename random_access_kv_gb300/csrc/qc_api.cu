@@ -186,6 +186,7 @@ int64_t qc_attend_workspace(const qc_ctx *ctx, int64_t n_seq, int n_nodes, int n
     if (!ctx || n_seq < 0 || n_seq > 65535 || n_nodes < 1 || n_nodes > qc::kMaxNodes) return -1;
     if (n_q_heads < 1 || n_q_heads % ctx->heads || n_q_heads / ctx->heads > qc::kMaxGroup) return -1;
     if (max_len < 0 || max_len > INT32_MAX - 2 * qc::kMaxNodes) return -1;
+    if (n_seq * n_nodes * n_q_heads > INT32_MAX) return -1;
     return qc::attend_workspace(ctx, n_seq, n_nodes, n_q_heads, max_len);
 }
 

@@ -1,11 +1,16 @@
 // Attention over the quantised cache for few query rows per key/value head (single tokens, chains,
 // small trees).
 //
-// What bounds it: the pages, read once. Each of the eight warps on an SM (two CTAs of four, so that every
-// scheduler has two) has a run of tiles of 32 places of its own. It copies them from the pages, as they lie, to its ring of shared-memory stages
-// with bulk asynchronous copies, two or more tiles ahead, and turns codes into tensor-core fragments in
-// registers. Warps never wait for one another; what one leaves unused of the memory's bandwidth, for
-// instance at the start of a job, the other seven on its SM take.
+// Each of the eight warps on an SM (two CTAs of four, so that every scheduler has two) has a run of tiles of
+// 32 places of its own. It copies them from the pages, as they lie, to its ring of shared-memory stages with
+// bulk asynchronous copies, two or more tiles ahead, and turns codes into tensor-core fragments in registers.
+// Warps never wait for one another; what one leaves unused of the memory's bandwidth, for instance at the
+// start of a job, the other seven on its SM take.
+//
+// What bounds it: in the limit the pages, read once. As measured the schedulers issue every second cycle, two
+// warps each, held up by the latency of dependent conversions and products: 4 rows over 32 sequences of up to
+// 32,768 places (e2m1, 637 MB) take 226 us, 2.8 TB/s; 20 rows over 16 x 16,384 (int8, 555 MB) 195 us. Twelve
+// warps of 168 registers instead of eight of 255 spill: 270 and 216 us when eight took 256 and 212.
 //
 // Products. Codes are exact in fp16, and so are e2m1 codes times their e4m3 block scale (5 bits), so
 // the products q . code are exact and summed in float32; the row's scale multiplies the score
