@@ -338,6 +338,7 @@ class CacheContext(Context):
 
 _QC_TYPES, _F32, _I32, _I64, _U8 = {}, None, None, None, None
 _raw_stream = None
+_NO_STRIDES = (0, 0, 1)
 
 
 def _qc_init() -> None:
@@ -347,10 +348,6 @@ def _qc_init() -> None:
     _QC_TYPES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
     _F32, _I32, _I64, _U8 = torch.float32, torch.int32, torch.int64, torch.uint8
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
-
-
-def _is(t, dtype, shape, dev: int) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
 def _refuse(ctx: CacheContext, **what):
@@ -392,32 +389,33 @@ def qc_page_bytes(ctx: CacheContext) -> int:
     return int(b)
 
 
-def _qc_stream(stream, dev: int):
-    return _raw_stream(dev) if stream is None else _stream(stream)
-
-
 def qc_norm_rope(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, rot: int, interleaved: bool, q_out, k_out,
                  stream=None) -> None:
     """q [n, hq, d] and k [n, hk, d] (either may be None), strided; w_q, w_k float32 [d] or None; pos int64
     [n]; table float32 [max_pos, rot]; q_out, k_out like q and k (themselves, too)."""
     dev, d = ctx.device, ctx.d
-    x = q if q is not None else k
-    if x is None:
+    ok, n, dtype = True, None, None
+    if q is not None:
+        qs, q0, o0 = q.shape, q.stride(), q_out.stride()
+        n, dtype = qs[0], q.dtype
+        ok = (len(qs) == 3 and qs[2] == d and q_out.dtype is dtype and q_out.shape == qs and q0[2] == 1 and o0[2] == 1
+              and q.get_device() == dev and q_out.get_device() == dev
+              and (w_q is None or (w_q.dtype is _F32 and w_q.shape == (d,) and w_q.get_device() == dev and w_q.is_contiguous())))
+    if k is not None and ok:
+        ks, k0, o1 = k.shape, k.stride(), k_out.stride()
+        if q is None:
+            n, dtype = ks[0], k.dtype
+        ok = (len(ks) == 3 and ks[0] == n and ks[2] == d and k.dtype is dtype and k_out.dtype is dtype and k_out.shape == ks
+              and k0[2] == 1 and o1[2] == 1 and k.get_device() == dev and k_out.get_device() == dev
+              and (w_k is None or (w_k.dtype is _F32 and w_k.shape == (d,) and w_k.get_device() == dev and w_k.is_contiguous())))
+    if n is None:
         raise ValueError("neither q nor k")
-    dtype, n = x.dtype, x.shape[0]
-    ok, args = dtype in _QC_TYPES, []
-    for x, out, w in ((q, q_out, w_q), (k, k_out, w_k)):
-        if x is None:
-            args.append((None, 0, 0, 0, None, None, 0, 0))
-            continue
-        shape, s, so = x.shape, x.stride(), out.stride()
-        ok = (ok and x.dtype is dtype and out.dtype is dtype and len(shape) == 3 and shape[0] == n and shape[2] == d and out.shape == shape
-              and s[2] == 1 and so[2] == 1 and x.get_device() == dev and out.get_device() == dev
-              and (w is None or _is(w, _F32, (d,), dev)))
-        if not ok:
-            break
-        args.append((x.data_ptr(), shape[1], s[0], s[1], None if w is None else w.data_ptr(), out.data_ptr(), so[0], so[1]))
-    if not ok or (rot and not (_is(pos, _I64, (n,), dev) and _is(table, _F32, (table.shape[0], rot), dev))):
+    if ok and rot:
+        most = table.shape[0]
+        ok = (pos.dtype is _I64 and pos.shape == (n,) and pos.get_device() == dev and pos.is_contiguous() and table.dtype is _F32
+              and table.shape == (most, rot) and table.get_device() == dev and table.is_contiguous())
+    kind = _QC_TYPES.get(dtype)
+    if not ok or kind is None:
         rows = {}
         for name, x, out, w in (("q", q, q_out, w_q), ("k", k, k_out, w_k)):
             if x is not None:
@@ -427,10 +425,21 @@ def qc_norm_rope(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, rot:
         if rot:
             rows.update(pos=(pos, _I64, (n,), True), table=(table, _F32, (None, rot), True))
         _refuse(ctx, **rows)
-    a, b = args
-    rc = lib().qc_norm_rope(ctx.handle, _QC_TYPES[dtype], n, *a[:5], *b[:5], eps, pos.data_ptr() if rot else None,
-                            table.data_ptr() if rot else None, table.shape[0] if rot else 0, rot, interleaved, *a[5:], *b[5:],
-                            _qc_stream(stream, dev))
+    if q is None:
+        q_in, q_to, hq, wq, q0, o0 = None, None, 0, None, _NO_STRIDES, _NO_STRIDES
+    else:
+        q_in, q_to, hq, wq = q.data_ptr(), q_out.data_ptr(), qs[1], None if w_q is None else w_q.data_ptr()
+    if k is None:
+        k_in, k_to, hk, wk, k0, o1 = None, None, 0, None, _NO_STRIDES, _NO_STRIDES
+    else:
+        k_in, k_to, hk, wk = k.data_ptr(), k_out.data_ptr(), ks[1], None if w_k is None else w_k.data_ptr()
+    if rot:
+        at, turns = pos.data_ptr(), table.data_ptr()
+    else:
+        at = turns = None
+        most = 0
+    rc = _lib.qc_norm_rope(ctx.handle, kind, n, q_in, hq, q0[0], q0[1], wq, k_in, hk, k0[0], k0[1], wk, eps, at, turns, most, rot, interleaved,
+                           q_to, o0[0], o0[1], k_to, o1[0], o1[1], _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         raise FQError("qc_norm_rope", rc)
 
@@ -440,12 +449,13 @@ def qc_write(ctx: CacheContext, k, v, slots, pages, stream=None) -> None:
     dev, shape, dtype = ctx.device, k.shape, k.dtype
     n, n_pages, sk, sv = shape[0], pages.shape[0], k.stride(), v.stride()
     if not (dtype in _QC_TYPES and v.dtype is dtype and shape == (n, ctx.n_heads, ctx.d) and v.shape == shape and sk[2] == 1 and sv[2] == 1
-            and k.get_device() == dev and v.get_device() == dev and _is(slots, _I64, (n,), dev)
-            and _is(pages, _U8, (n_pages, ctx.page_bytes), dev)):
+            and k.get_device() == dev and v.get_device() == dev
+            and slots.dtype is _I64 and slots.shape == (n,) and slots.get_device() == dev and slots.is_contiguous()
+            and pages.dtype is _U8 and pages.shape == (n_pages, ctx.page_bytes) and pages.get_device() == dev and pages.is_contiguous()):
         _refuse(ctx, k=(k, None, (n, ctx.n_heads, ctx.d), False), v=(v, dtype, (n, ctx.n_heads, ctx.d), False),
                 slots=(slots, _I64, (n,), True), pages=(pages, _U8, (None, ctx.page_bytes), True))
-    rc = lib().qc_write(ctx.handle, _QC_TYPES[dtype], n, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], slots.data_ptr(),
-                        pages.data_ptr(), n_pages, _qc_stream(stream, dev))
+    rc = _lib.qc_write(ctx.handle, _QC_TYPES[dtype], n, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], slots.data_ptr(),
+                       pages.data_ptr(), n_pages, _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         raise FQError("qc_write", rc)
 
@@ -457,12 +467,16 @@ def qc_read(ctx: CacheContext, pages, slots, k_out, v_out, stream=None) -> None:
     if out is None:
         return
     dtype, shape = out.dtype, (n, ctx.n_heads, ctx.d)
-    if not (dtype in _QC_TYPES and (k_out is None or _is(k_out, dtype, shape, dev)) and (v_out is None or _is(v_out, dtype, shape, dev))
-            and _is(slots, _I64, (n,), dev) and _is(pages, _U8, (n_pages, ctx.page_bytes), dev)):
+    if not (dtype in _QC_TYPES
+            and (k_out is None or (k_out.dtype is dtype and k_out.shape == shape and k_out.get_device() == dev and k_out.is_contiguous()))
+            and (v_out is None or (v_out.dtype is dtype and v_out.shape == shape and v_out.get_device() == dev and v_out.is_contiguous()))
+            and slots.dtype is _I64 and slots.shape == (n,) and slots.get_device() == dev and slots.is_contiguous()
+            and pages.dtype is _U8 and pages.shape == (n_pages, ctx.page_bytes) and pages.get_device() == dev and pages.is_contiguous()):
         _refuse(ctx, slots=(slots, _I64, (n,), True), pages=(pages, _U8, (None, ctx.page_bytes), True),
                 k_out=(k_out, None, shape, True), v_out=(v_out, dtype, shape, True))
-    rc = lib().qc_read(ctx.handle, _QC_TYPES[dtype], n, slots.data_ptr(), pages.data_ptr(), n_pages,
-                       None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), _qc_stream(stream, dev))
+    rc = _lib.qc_read(ctx.handle, _QC_TYPES[dtype], n, slots.data_ptr(), pages.data_ptr(), n_pages,
+                      None if k_out is None else k_out.data_ptr(), None if v_out is None else v_out.data_ptr(),
+                      _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         raise FQError("qc_read", rc)
 
@@ -477,22 +491,29 @@ def qc_attend(ctx: CacheContext, pages, q, table, lens, nodes, tree, scale: floa
         raise ValueError(f"q is {tuple(shape)}, not [n_seq, n_nodes, n_q_heads, {d}]")
     n_seq, n_nodes, hq, _ = shape
     n_pages, sq, st, width = pages.shape[0], q.stride(), table.stride(), table.shape[-1]
-    if not (shape[3] == d and sq[3] == 1 and q.get_device() == dev and dtype in _QC_TYPES and _is(out, dtype, shape, dev)
+    if not (shape[3] == d and sq[3] == 1 and q.get_device() == dev and dtype in _QC_TYPES
+            and out.dtype is dtype and out.shape == shape and out.get_device() == dev and out.is_contiguous()
             and table.dtype is _I32 and table.shape == (n_seq, width) and (st[1] == 1 or width == 1) and table.get_device() == dev
-            and _is(lens, _I32, (n_seq,), dev) and (nodes is None or _is(nodes, _I32, (n_seq,), dev))
-            and (tree is None or _is(tree, _I32, (n_seq, n_nodes, (n_nodes + 31) // 32), dev))
-            and (lse is None or _is(lse, _F32, (n_seq, n_nodes, hq), dev))
-            and _is(pages, _U8, (n_pages, ctx.page_bytes), dev) and _is(workspace, _U8, workspace.shape, dev)):
+            and lens.dtype is _I32 and lens.shape == (n_seq,) and lens.get_device() == dev and lens.is_contiguous()
+            and (nodes is None
+                 or (nodes.dtype is _I32 and nodes.shape == (n_seq,) and nodes.get_device() == dev and nodes.is_contiguous()))
+            and (tree is None or (tree.dtype is _I32 and tree.shape == (n_seq, n_nodes, (n_nodes + 31) // 32) and tree.get_device() == dev
+                                  and tree.is_contiguous()))
+            and (lse is None
+                 or (lse.dtype is _F32 and lse.shape == (n_seq, n_nodes, hq) and lse.get_device() == dev and lse.is_contiguous()))
+            and pages.dtype is _U8 and pages.shape == (n_pages, ctx.page_bytes) and pages.get_device() == dev and pages.is_contiguous()
+            and workspace.dtype is _U8 and workspace.get_device() == dev and workspace.is_contiguous()):
         _refuse(ctx, q=(q, None, (n_seq, n_nodes, hq, d), False), out=(out, dtype, (n_seq, n_nodes, hq, d), True),
                 table=(table, _I32, (n_seq, None), False), lens=(lens, _I32, (n_seq,), True), nodes=(nodes, _I32, (n_seq,), True),
                 tree=(tree, _I32, (n_seq, n_nodes, (n_nodes + 31) // 32), True), lse=(lse, _F32, (n_seq, n_nodes, hq), True),
                 pages=(pages, _U8, (None, ctx.page_bytes), True), workspace=(workspace, _U8, (None,), True))
     if -(-(max_len + n_nodes) // ctx.page_tokens) > width:       # a row's width, which its stride may exceed
         raise FQError("qc_attend", FQ_EINVAL)
-    rc = lib().qc_attend(ctx.handle, _QC_TYPES[dtype], n_seq, n_nodes, hq, q.data_ptr(), sq[0], sq[1], sq[2], table.data_ptr(),
-                         st[0] if n_seq > 1 else max(st[0], width), lens.data_ptr(), None if nodes is None else nodes.data_ptr(),
-                         None if tree is None else tree.data_ptr(), pages.data_ptr(), n_pages, scale, max_len, out.data_ptr(),
-                         None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(), _qc_stream(stream, dev))
+    rc = _lib.qc_attend(ctx.handle, _QC_TYPES[dtype], n_seq, n_nodes, hq, q.data_ptr(), sq[0], sq[1], sq[2], table.data_ptr(),
+                        st[0] if n_seq > 1 else max(st[0], width), lens.data_ptr(), None if nodes is None else nodes.data_ptr(),
+                        None if tree is None else tree.data_ptr(), pages.data_ptr(), n_pages, scale, max_len, out.data_ptr(),
+                        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                        _raw_stream(dev) if stream is None else _stream(stream))
     if rc:
         raise FQError("qc_attend", rc)
 

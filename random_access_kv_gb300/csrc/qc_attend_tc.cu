@@ -34,7 +34,9 @@ namespace {
 
 using namespace fq::sm100;
 
-constexpr float kLag = 3.f;             // how far (base 2) a score may pass the row's reference
+// A score may pass the row's reference by kLag (base 2), which is what fp16 holds; one that passes it by kSoon has
+// the reference moved with the next half tile, which costs the sums' rescaling but no second sweep.
+constexpr float kLag = 3.9f, kSoon = 2.f;
 constexpr float kHead = 3.f;            // how far above the largest score a new reference is put
 constexpr int kTop = 12;                // weights' unit: 2^12 over the scales' bound
 constexpr int kMostRaw = 8;
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             float m = -INFINITY, ref = 0.f;
             int e = 0;                          // log2 of the weights' unit
             float2 l = make_float2(0.f, 0.f);
+            float soon = -INFINITY;             // the row's next reference, where one waits
             for (int tile = run.from; ok && tile < run.end; ++tile, ++it) {
                 for (int half = 0; half < 2; ++half) {
                     const int buf = 2 * rt + half, place = tile * kTile + 64 * half;
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         uint32_t pw[32];
                         float2 sum;
                         float top;
-                        // one pass with the reference as it is; a second if a score or a scale has passed it
+                        // one pass with the reference as it is; a second if a score or a scale has passed it too far
                         auto sweep = [&](auto masked) {
                             constexpr bool kMasked = decltype(masked)::value;
                             const float mm = (m == -INFINITY ? 0.f : m) - (float)e;
@@ -295,39 +298,51 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                             top = fmaxf(top, top1);
                             sum = add2f(sum, sum1);
                         };
+                        // the sums so far, in another unit
+                        auto rescale = [&](float by) {
+                            ok = warp_wait(&bar.o_done[rt], 2 * it + half - 1);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                const uint32_t at = tmem + lanes + 256 + rt * 128 + 32 * c;
+                                tmem_ld32_nowait(at, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                                tmem_st32(at, o);
+                            }
+                        };
+                        const bool sums = tile > run.from || half;      // there are some
+                        float by = 1.f;
+                        bool moved = __any_sync(0xffffffffu, soon > m);
+                        if (moved) {
+                            const float m2 = fmaxf(soon, m);
+                            by = m2 == m ? 1.f : ex2(m - m2);
+                            m = m2;
+                        }
                         for (int pass = 0;; ++pass) {
                             if (mask)
                                 sweep(std::true_type{});
                             else
                                 sweep(std::false_type{});
-                            if (pass) break;
                             top *= down;
-                            if (!__any_sync(0xffffffffu, top > m + kLag || vtop > ref)) break;
+                            if (pass || !__any_sync(0xffffffffu, top > m + kLag || vtop > ref)) break;
                             const float m2 = top > m + kLag ? top + kHead : m;
                             const float ref2 = fmaxf(ref, fmaxf(power_above(vtop), 3.2311742677852644e-27f));     // at least 2^-88
                             const int e2 = kTop + 127 - (int)(__float_as_uint(ref2) >> 23);
-                            // sums so far in the new unit
-                            const float by = m == -INFINITY ? 0.f : ex2(m - m2 + (float)(e2 - e));
-                            l.x *= by;
-                            l.y *= by;
-                            if (tile > run.from || half) {
-                                ok = warp_wait(&bar.o_done[rt], 2 * it + half - 1);
-                                tc_fence_after();
-#pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
-                                    uint32_t o[32];
-                                    const uint32_t at = tmem + lanes + 256 + rt * 128 + 32 * c;
-                                    tmem_ld32_nowait(at, o);
-                                    tmem_wait_ld();
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-                                    tmem_st32(at, o);
-                                }
-                            }
+                            by = m == -INFINITY ? 0.f : by * ex2(m - m2 + (float)(e2 - e));
+                            moved = true;
                             m = m2;
                             ref = ref2;
                             e = e2;
                         }
+                        if (moved) {
+                            l.x *= by;
+                            l.y *= by;
+                            if (sums) rescale(by);
+                        }
+                        soon = top > m + kSoon ? top + kHead : -INFINITY;
                         l = add2f(l, sum);
                         tmem_st32(s_at, pw);
                         tmem_wait_st();
