@@ -114,23 +114,26 @@ cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_t
 namespace {
 
 // Which kernel. qc_attend_tc.cu pays 128 rows' tensor-core time and one thread's softmax per row whatever the
-// rows' number, qc_attend_rows.cu its conversion and products anew for every 32 rows: the first is for more
+// rows' number, qc_attend_rows.cuh its conversion and products anew for every 32 rows: the first is for more
 // than 32. Below about a thousand places a head's tiles of 128 are too few to hide its pipeline's start, and
-// rows whose weight lies on few places are likely, which qc_attend_rows.cu follows to the last bit.
-//   e4m3, d = 64, 128 rows, 8 sequences of 4,096 places at most: 31 us here, 57 us with qc_attend_rows.cu;
-//   int8, d = 128, 256 rows, 8 x 32,768: 0.39 ms and 1.6 ms; 20 rows, 16 x 16,384: 225 us and 212 us;
-//   e2m1, d = 128, 4 rows, 32 sequences of 32,768 at most: 0.49 ms and 0.23 ms.
+// rows whose weight lies on few places are likely, which qc_attend_rows.cuh follows to the last bit.
+//   e4m3, d = 64, 128 rows, 8 sequences of 4,096 places at most: 31 us here, 57 us with 32 rows a warp there;
+//   int8, d = 128, 256 rows, 8 x 32,768: 0.38 ms and 1.6 ms; 20 rows, 16 x 16,384: 225 us and 169 us;
+//   e2m1, d = 128, 4 rows, 32 sequences of 32,768 at most: 0.49 ms and 0.16 ms.
 bool many_rows(int64_t max_len, int n_nodes, int rows) { return rows > 32 && max_len + n_nodes >= 1024; }
 
 }  // namespace
 
 int64_t attend_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {
-    return many_rows(max_len, n_nodes, n_nodes * (n_q_heads / c->heads)) ? tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len)
-                                                                         : rows_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
+    const int rows = n_nodes * (n_q_heads / c->heads);
+    if (n_seq == 0) return 0;
+    if (many_rows(max_len, n_nodes, rows)) return tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
+    return c->d == 64 ? rows_workspace_d<64>(c, rows, n_seq, n_nodes, max_len) : rows_workspace_d<128>(c, rows, n_seq, n_nodes, max_len);
 }
 
 cudaError_t launch_attend(const qc_ctx *c, int type, const Attend &p, cudaStream_t s) {
-    return many_rows(p.max_len, p.n_nodes, p.n_nodes * p.group) ? launch_attend_tc(c, type, p, s) : launch_attend_rows(c, type, p, s);
+    if (many_rows(p.max_len, p.n_nodes, p.n_nodes * p.group)) return launch_attend_tc(c, type, p, s);
+    return c->d == 64 ? attend_rows_d<64>(c, type, p, s) : attend_rows_d<128>(c, type, p, s);
 }
 
 }  // namespace qc

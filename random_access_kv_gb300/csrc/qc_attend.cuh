@@ -160,9 +160,19 @@ inline cudaError_t allow_smem(Kernel *kernel, int bytes, int device, std::atomic
 // Joins the parts of every job that lies in several units, and writes the zeros of sequences without tiles.
 cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_tiles, int tile, int units, cudaStream_t s);
 
-// The kernels (qc_attend_rows.cu, qc_attend_tc.cu).
-cudaError_t launch_attend_rows(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
-int64_t rows_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len);
+// The kernels (qc_attend_rows.cuh, qc_attend_tc.cu).
+template <int D>
+cudaError_t attend_rows_d(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
+template <int D>
+int64_t rows_workspace_d(const qc_ctx *c, int rows, int64_t n_seq, int n_nodes, int64_t max_len);
+template <>
+cudaError_t attend_rows_d<64>(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
+template <>
+cudaError_t attend_rows_d<128>(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
+template <>
+int64_t rows_workspace_d<64>(const qc_ctx *c, int rows, int64_t n_seq, int n_nodes, int64_t max_len);
+template <>
+int64_t rows_workspace_d<128>(const qc_ctx *c, int rows, int64_t n_seq, int n_nodes, int64_t max_len);
 cudaError_t launch_attend_tc(const qc_ctx *c, int type, const Attend &p, cudaStream_t s);
 int64_t tc_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len);
 

@@ -17,7 +17,7 @@
 // heads). A tile's half of 64 scores takes a softmax warp about 1,800 cycles, a row operand's conversion a
 // warp about 1,300; a moved reference does the half anew and rescales the row's sums.
 //
-// Arithmetic is that of qc_attend_rows.cu: exact products of fp16 operands, float32 sums; weights relative
+// Arithmetic is that of qc_attend_rows.cuh: exact products of fp16 operands, float32 sums; weights relative
 // to a reference that moves only when a score passes it by 2^3, to 2^3 above that score, times the values' row
 // scale, in fp16. Their unit is a power of two (2^12 over the bound of the values' scales) and is folded into
 // the exponent, so the running sum l is in that unit too. fp16 holds a weight to 11 bits down to 2^-14, that is
