@@ -52,7 +52,10 @@ constexpr float kHead = 3.f;            // how far above the largest score a new
 constexpr float kLeastNormal = 6.103515625e-05f;    // 2^-14, fp16's
 constexpr float kLift = 16777216.f;     // 2^24
 constexpr float kHeavy = 2.44140625e-04f;   // 2^-12
-constexpr int kSettled = 12;            // heavy places that a row must have met
+// Heavy places that a row must have met: so many that no element is zero in all of them. About one in six
+// e2m1 codes is a zero, one in fifty of int8's, one in thousands of e4m3's.
+template <int FMT>
+constexpr int kSettled = FMT == QC_E2M1 ? 12 : FMT == QC_INT8 ? 5 : 3;
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -390,7 +393,7 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
         }
     }
     // Weights below fp16's normals are off by up to 2^-25, which shows only where all heavier places hold
-    // an exact zero. Once a row has met a dozen places of weight 2^-12 or more since its reference last
+    // an exact zero. Once a row has met kSettled places of weight 2^-12 or more since its reference last
     // moved, no element has only zeros in them and the error is below 2^-11 of the sum. Until then, what
     // the rounding of light weights leaves is added in a pass of its own, scaled up, with the sums scaled
     // along (powers of two: exact).
@@ -411,8 +414,8 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
                 }
                 k = min(column_sum(k) + ((z.heavy[n] >> (16 * e)) & 0xff), 127);
                 z.heavy[n] = (z.heavy[n] & ~(0xff << (16 * e))) | k << (16 * e);
-                few |= k < kSettled;
-                light |= k < kSettled && least < kLeastNormal;
+                few |= k < kSettled<FMT>;
+                light |= k < kSettled<FMT> && least < kLeastNormal;
             }
         }
         light = __any_sync(0xffffffffu, light);
