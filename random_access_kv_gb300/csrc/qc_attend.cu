@@ -117,9 +117,9 @@ namespace {
 // rows' number, qc_attend_rows.cuh its conversion and products anew for every 32 rows: the first is for more
 // than 32. Below about a thousand places a head's tiles of 128 are too few to hide its pipeline's start, and
 // rows whose weight lies on few places are likely, which qc_attend_rows.cuh follows to the last bit.
-//   e4m3, d = 64, 128 rows, 8 sequences of 4,096 places at most: 31 us here, 57 us with 32 rows a warp there;
-//   int8, d = 128, 256 rows, 8 x 32,768: 0.38 ms and 1.6 ms; 20 rows, 16 x 16,384: 225 us and 169 us;
-//   e2m1, d = 128, 4 rows, 32 sequences of 32,768 at most: 0.49 ms and 0.16 ms.
+//   e4m3, d = 64, 128 rows, 8 sequences of 4,096 places at most: 32 us here, 57 us there;
+//   int8, d = 128, 256 rows, 8 x 32,768: 0.38 ms and 1.6 ms; 20 rows, 16 x 16,384: 225 us and 167 us;
+//   e2m1, d = 128, 4 rows, 32 sequences of 32,768 at most: 0.49 ms and 0.17 ms (one-term weights).
 bool many_rows(int64_t max_len, int n_nodes, int rows) { return rows > 32 && max_len + n_nodes >= 1024; }
 
 }  // namespace

@@ -8,10 +8,10 @@
 // others on its SM take.
 //
 // What bounds it: in the limit the pages, read once; as measured the latency of dependent conversions and
-// products, two to three warps a scheduler. 4 rows over 32 sequences of up to 32,768 places (e2m1, 637 MB) take
-// 159 us (4.0 TB/s, 59 % of the card's copy rate), 20 rows over 16 x 16,384 (int8, 555 MB) 169 us (3.3 TB/s).
-// With queries as the products' 16 rows and places as their 8 columns, twice the registers for the outputs of
-// up to 8 queries and eight warps on an SM, it was 226 and 195 us.
+// products, two to three warps a scheduler. 4 rows over 32 sequences of up to 32,768 places (e2m1, fp16 queries, 637 MB)
+// take 182 us (3.5 TB/s, 52 % of the card's copy rate), 20 rows over 16 x 16,384 (int8, bf16 queries, 555 MB) 167
+// us (3.3 TB/s). With queries as the products' 16 rows and places as their 8 columns, twice the registers for the
+// outputs of up to 8 queries and eight warps on an SM, it was 226 and 195 us.
 //
 // Products. Places are the products' 16 rows and queries their 8 columns (S^T = K Q^T, O^T = V^T P^T): the
 // conversion, which costs most, goes over places, and few queries leave few columns empty. NT column tiles
@@ -22,7 +22,7 @@
 // running bound of the scales seen. A row's reference m moves only when a score passes it by 3 (base 2), to 3
 // above that score: so p_t <= 2^3 and w_t <= 2^15, the sums are rescaled seldom (a first tile's reference
 // serves until a score is 2^6 times heavier), and the maximum is only reduced over the lanes when it is. w_t
-// keeps fp16's 11 bits down to 2^-14; `add_tile` says what becomes of lighter weights.
+// keeps fp16's 11 bits down to 2^-14; `add_tile` says what becomes of lighter weights, and of the other bits.
 //
 // Order of elements. A sum over d may take them in any order as long as both operands do: lane c of a quad
 // takes elements c d / 4 .. of a key, so one 16-byte load feeds four (e2m1: eight) steps. For the values lane
@@ -208,11 +208,11 @@ __device__ __forceinline__ void scores(const unsigned char *st, const Offsets<FM
     }
 }
 
-// out[n][j] += the values of half tile x times weights p[n][x]; j: elements g D / 8 + 2 j and 2 j + 1. keep: which of
+// out[n][j] += the values of half tile x times weights p[0][n][x] (+ p[1][n][x]); j: elements g D / 8 + 2 j and 2 j + 1. keep: which of
 // the eight places that the lane loads exist (only asked when MASK; the others' bytes may be anything, NaN
 // codes included, and count as zeros).
-template <int FMT, int D, int NT, bool MASK>
-__device__ __forceinline__ void add_values(const unsigned char *st, const Offsets<FMT, D> &o, const uint32_t (&p)[NT][2][2], int lane,
+template <int FMT, int D, int NT, int TERMS, bool MASK>
+__device__ __forceinline__ void add_values(const unsigned char *st, const Offsets<FMT, D> &o, const uint32_t (&p)[TERMS][NT][2][2], int lane,
                                            uint32_t keep, float (&out)[NT][D / 16][4]) {
     using S = Shape<FMT, D>;
     constexpr int W = S::kRow / 32;                     // words of a place in a lane
@@ -231,7 +231,9 @@ __device__ __forceinline__ void add_values(const unsigned char *st, const Offset
         auto add = [&](int j, uint32_t lo0, uint32_t lo1, uint32_t hi0, uint32_t hi1) {
             const uint32_t a[4] = {lo0, lo1, hi0, hi1};
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma(out[n][j], a, p[n][x][0], p[n][x][1]);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) mma(out[n][j], a, p[t][n][x][0], p[t][n][x][1]);
         };
         if constexpr (FMT == QC_E2M1) {
             uint32_t sb[2];
@@ -322,7 +324,7 @@ struct Seen {
     uint32_t row[NT], there, keep;
 };
 
-template <int FMT, int D, int NT, bool MASK>
+template <int FMT, int D, int NT, int TERMS, bool MASK>
 __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<FMT, D> &of, const uint32_t (&q)[NT][D / 16][2], float up,
                                          const float (&down)[NT][2], const Seen<NT> &seen, int lane, State<D, NT> &z) {
     using S = Shape<FMT, D>;
@@ -421,16 +423,28 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
         light = __any_sync(0xffffffffu, light);
         z.settled = !__any_sync(0xffffffffu, few);
     }
-    uint32_t p[NT][2][2];
+    // A weight to 11 bits, and for fp16 outputs what that leaves, to 22. With 11 an fp16 output was 1.3 to 1.7 times
+    // as far from 64 bits as its own rounding is; bf16's eight bits hide it. (One token over 32 ragged sequences,
+    // e2m1: 170 us with one term, 182 with two.)
+    uint32_t p[TERMS][NT][2][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) p[n][x][u] = transpose8(pack2(s[n][x][2 * u], s[n][x][2 * u + 1]));
+            for (int u = 0; u < 2; ++u) {
+                float &w0 = s[n][x][2 * u], &w1 = s[n][x][2 * u + 1];
+#pragma unroll
+                for (int t = 0; t < TERMS; ++t) {
+                    const uint32_t h = pack2(w0, w1);
+                    p[t][n][x][u] = transpose8(h);
+                    const float2 had = float2_of(h);
+                    if (t + 1 < TERMS) w0 -= had.x, w1 -= had.y;
+                }
+            }
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
-        add_values<FMT, D, NT, MASK>(st, of, p, lane, seen.keep, z.o);
+        add_values<FMT, D, NT, TERMS, MASK>(st, of, p, lane, seen.keep, z.o);
         if (!light) break;
         const float by = pass ? 1.f / kLift : kLift;
 #pragma unroll
@@ -444,9 +458,12 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
             for (int x = 0; x < 2; ++x)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
+                    // what the terms leave of the light ones
                     const float w0 = s[n][x][2 * u], w1 = s[n][x][2 * u + 1];
+                    const bool l0 = fabsf(w0) < kLeastNormal, l1 = fabsf(w1) < kLeastNormal;
                     const float2 had = float2_of(pack2(w0, w1));
-                    p[n][x][u] = transpose8(pack2(w0 < kLeastNormal ? (w0 - had.x) * kLift : 0.f, w1 < kLeastNormal ? (w1 - had.y) * kLift : 0.f));
+                    p[0][n][x][u] = transpose8(pack2(l0 ? (w0 - had.x) * kLift : 0.f, l1 ? (w1 - had.y) * kLift : 0.f));
+                    if (TERMS == 2) p[TERMS - 1][n][x][u] = 0;
                 }
     }
 }
@@ -569,6 +586,7 @@ __device__ __forceinline__ Seen<NT> look(const Attend &p, const Walk &w, int t0,
 template <typename T, int FMT, int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const Attend p, const Parts parts, const Plan plan) {
     using S = Shape<FMT, D>;
+    constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 1;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t bars[kWarps][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, unit = blockIdx.x * kWarps + warp;
@@ -625,9 +643,9 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const 
             const int t0 = tile * kTile;
             const uint32_t b = (bad >> (2 * stage)) & 3u;
             if (t0 + kTile <= w.n.x && !b) {
-                add_tile<FMT, D, NT, false>(st, of, q, up, down, Seen<NT>{}, lane, z);
+                add_tile<FMT, D, NT, kTerms, false>(st, of, q, up, down, Seen<NT>{}, lane, z);
             } else {
-                add_tile<FMT, D, NT, true>(st, of, q, up, down, look<FMT, D, NT>(p, w, t0, b, r0, R, lane), lane, z);
+                add_tile<FMT, D, NT, kTerms, true>(st, of, q, up, down, look<FMT, D, NT>(p, w, t0, b, r0, R, lane), lane, z);
             }
             __syncwarp();
             if (++stage == plan.stages) stage = 0, phase ^= 1u;

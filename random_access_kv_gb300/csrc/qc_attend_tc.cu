@@ -19,7 +19,7 @@
 //
 // Arithmetic is that of qc_attend_rows.cuh: exact products of fp16 operands, float32 sums; weights relative
 // to a reference that moves only when a score passes it by 2^3, to 2^3 above that score, times the values' row
-// scale, in fp16. Their unit is a power of two (2^12 over the bound of the values' scales) and is folded into
+// scale, in fp16 (two of them for fp16 outputs). Their unit is a power of two (2^12 over the bound of the values' scales) and is folded into
 // the exponent, so the running sum l is in that unit too. fp16 holds a weight to 11 bits down to 2^-14, that is
 // 2^-23 of the heaviest or less: lighter ones are not followed further here, where prefixes are long. (A
 // reference 2^9 above the score moves less often, 0.36 instead of 0.39 ms for 256 rows over 8 x 32,768, and
@@ -70,6 +70,10 @@ struct Plan {
 template <typename T, int FMT, int D, int NM>
 __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(const Attend p, const Parts parts, const Plan plan) {
     using I = Item<FMT, D>;
+    // A weight to 11 bits, and for fp16 outputs what that leaves, to 22: with 11 an fp16 output was 1.5 to 1.7 times
+    // as far from 64 bits as its own rounding is, bf16's eight bits hide it. (Trees of 16, e4m3: 31.5 us with one
+    // term, 35.3 with two.)
+    constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 1;
     constexpr int kOp = kOperand<D>, kSoft = 4 * NM, kConv = kSoft, kProducer = kSoft + 4, kMma = kProducer + kProducers;
     extern __shared__ __align__(1024) unsigned char smem[];
     unsigned char *q_op = smem, *k_op = q_op + NM * kOp, *v_op = k_op + kOp, *raw = v_op + 2 * kOp;
@@ -178,9 +182,9 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             auto values = [&](int rt, int h, int vb, bool first) {      // O[rt] (+)= P[rt][h] V[vb][half h]
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4 * kTerms; ++k)         // the weights' terms one after the other
                     mma_f16_ts(tmem + 256 + rt * 128, tmem + (2 * rt + h) * 64 + 8 * k,
-                               sdesc_sw128_mn(va + vb * kOp + (4 * h + k) * 2048, kTile * 128), pv, !first || k > 0);
+                               sdesc_sw128_mn(va + vb * kOp + (4 * h + (k & 3)) * 2048, kTile * 128), pv, !first || k > 0);
                 mma_commit(&bar.o_done[rt]);
                 if (rt == NM - 1 && h == 1) mma_commit(&bar.v_free[vb]);
             };
@@ -247,7 +251,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         const bool mask = place + 64 > w.n.x || (ex.x & ex.y) != 0xffffffffu;
                         const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
                         const uint32_t s_at = tmem + lanes + buf * 64;
-                        uint32_t pw[32];
+                        uint32_t pw[32 * kTerms];
                         float2 sum;
                         float top;
                         // one pass with the reference as it is; a second if a score or a scale has passed it too far
@@ -293,6 +297,11 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                                     b = mul2f(b, make_float2(vs.z, vs.w));
                                     pw[16 * c + i / 2] = pack2(a.x, a.y);
                                     pw[16 * c + i / 2 + 1] = pack2(b.x, b.y);
+                                    if constexpr (kTerms == 2) {
+                                        const float2 ha = float2_of(pw[16 * c + i / 2]), hb = float2_of(pw[16 * c + i / 2 + 1]);
+                                        pw[32 + 16 * c + i / 2] = pack2(a.x - ha.x, a.y - ha.y);
+                                        pw[32 + 16 * c + i / 2 + 1] = pack2(b.x - hb.x, b.y - hb.y);
+                                    }
                                 }
                             }
                             top = fmaxf(top, top1);
@@ -345,6 +354,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         soon = top > m + kSoon ? top + kHead : -INFINITY;
                         l = add2f(l, sum);
                         tmem_st32(s_at, pw);
+                        if constexpr (kTerms == 2) tmem_st32(s_at + 32, pw + 32);
                         tmem_wait_st();
                         tc_fence_before();
                     }
