@@ -1,5 +1,5 @@
-// Attention over the quantised cache for many query rows per key/value head or long prefixes: products
-// on the fifth-generation tensor cores.
+// Attention over the quantised cache for many query rows per key/value head over long prefixes: products on
+// the fifth-generation tensor cores.
 //
 // One CTA per SM; NM row tiles of 128 query rows, tiles of 128 places. Roles:
 //   producer (3 warps)   copies keys' or values' codes and scales of a tile, as the pages hold them, to a
@@ -12,18 +12,17 @@
 // Scores and weights of a tile are two halves of 64 places, a buffer each: while a half's softmax runs, the
 // tensor cores take the other half's weights and make the next tile's scores.
 //
-// What bounds it: the softmax's and the conversion's issue slots and latency, with 256 rows 707 TFLOP/s of the
-// two products (37 % of a large matrix product's rate; 0.39 ms for 256 rows over 8 x 32,768 int8 places, 8
-// heads). A tile's half of 64 scores takes a softmax warp about 1,800 cycles, a row operand's conversion a
-// warp about 1,300; a moved reference does the half anew and rescales the row's sums.
+// What bounds it: the softmax's and the conversion's issue slots and latency, with 256 rows 727 TFLOP/s of the
+// two products (38 % of a large matrix product's rate; 0.38 ms for 256 bf16 rows over 8 x 32,768 int8 places, 8
+// heads). A tile's half of 64 scores takes a softmax warp about 1,800 cycles, an operand's conversion a warp
+// about 1,300.
 //
-// Arithmetic is that of qc_attend_rows.cuh: exact products of fp16 operands, float32 sums; weights relative
-// to a reference that moves only when a score passes it by 2^3, to 2^3 above that score, times the values' row
-// scale, in fp16 (two of them for fp16 outputs). Their unit is a power of two (2^12 over the bound of the values' scales) and is folded into
-// the exponent, so the running sum l is in that unit too. fp16 holds a weight to 11 bits down to 2^-14, that is
-// 2^-23 of the heaviest or less: lighter ones are not followed further here, where prefixes are long. (A
-// reference 2^9 above the score moves less often, 0.36 instead of 0.39 ms for 256 rows over 8 x 32,768, and
-// leaves 2^-17.)
+// Arithmetic is that of qc_attend_rows.cuh: exact products of fp16 operands, float32 sums; weights relative to a
+// reference that is put 2^3 above a score that passes it, times the values' row scale, in fp16 (two of them for
+// fp16 outputs). Their unit is a power of two (2^12 over the bound of the values' scales) and is folded into the
+// exponent, so the running sum l is in that unit too. fp16 holds a weight to 11 bits down to 2^-14, that is 2^-23
+// of the heaviest or less: lighter ones are not followed further here, where prefixes are long. (A reference 2^9
+// above the score moves less often, 0.36 instead of 0.39 ms at 256 rows, and leaves 2^-17.)
 #include <math.h>
 
 #include "qc_attend.cuh"
