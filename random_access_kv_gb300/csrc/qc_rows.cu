@@ -23,14 +23,14 @@ __device__ __forceinline__ int code_at(const Geometry &g, int which, int t, int 
 }
 
 // What a block works on: blockIdx.x = (token group, head), blockIdx.y = keys or values.
-template <int D, int U>
-struct Task {
-    static constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+template <int D, int U, int E>
+struct Task {               // E elements of a row to a lane
+    static constexpr int kLanes = D / E, kRows = 32 / kLanes;
     int lane, e0, h;
     int64_t token;          // of u = 0; the next ones kRows apart
     __device__ __forceinline__ Task(const Rows &p) {
         lane = threadIdx.x & 31;
-        e0 = lane % kLanes * 8;
+        e0 = lane % kLanes * E;
         const uint32_t group = blockIdx.x / (uint32_t)p.g.heads;
         h = (int)(blockIdx.x - group * (uint32_t)p.g.heads);
         token = ((int64_t)group * (kThreads / 32) + (threadIdx.x >> 5)) * (U * kRows) + lane / kLanes;
@@ -39,7 +39,7 @@ struct Task {
 
 template <typename T, int D, int FMT, int U>
 __global__ void __launch_bounds__(kThreads) write_rows(const Rows p) {
-    const Task<D, U> k(p);
+    const Task<D, U, 8> k(p);
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
     const int which = blockIdx.y, e0 = k.e0;
     const T *x = static_cast<const T *>(which ? p.v : p.k) + k.h * (which ? p.v_head : p.k_head) + e0;
@@ -109,10 +109,11 @@ __global__ void __launch_bounds__(kThreads) write_rows(const Rows p) {
     }
 }
 
+// A lane takes 16 elements here (a 16-byte piece, or a block of e2m1): twice the bytes under way of eight.
 template <typename T, int D, int FMT, int U>
 __global__ void __launch_bounds__(kThreads) read_rows(const Rows p) {
-    const Task<D, U> k(p);
-    constexpr int kRows = 32 / (D / 8);
+    const Task<D, U, 16> k(p);
+    constexpr int kRows = 32 / (D / 16);
     const int which = blockIdx.y, e0 = k.e0;
     T *out = static_cast<T *>(which ? p.v_out : p.k_out);
     if (!out) return;
@@ -122,12 +123,12 @@ __global__ void __launch_bounds__(kThreads) read_rows(const Rows p) {
         const int64_t token = k.token + u * kRows;
         slots[u] = token < p.n ? __ldg(p.slots + token) : -1;
     }
-    uint2 c[U];
+    uint4 c[U];
     uint32_t block[U];
     float scale[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        c[u] = make_uint2(0, 0);
+        c[u] = make_uint4(0, 0, 0, 0);
         block[u] = 0;
         scale[u] = 0.f;
         if (slots[u] >= 0 && slots[u] < p.slots_end) {
@@ -135,10 +136,11 @@ __global__ void __launch_bounds__(kThreads) read_rows(const Rows p) {
             const int t = (int)(slots[u] & (p.g.page - 1));
             const unsigned char *at = part + code_at<FMT>(p.g, which, t, e0);
             if constexpr (FMT == QC_E2M1) {
-                c[u].x = *reinterpret_cast<const uint32_t *>(at);
+                const uint2 w = *reinterpret_cast<const uint2 *>(at);
+                c[u].x = w.x, c[u].y = w.y;
                 block[u] = part[p.g.block_scales(which) + t * p.g.blocks + e0 / 16];
             } else {
-                c[u] = *reinterpret_cast<const uint2 *>(at);
+                c[u] = *reinterpret_cast<const uint4 *>(at);
             }
             scale[u] = reinterpret_cast<const float *>(part + p.g.scales(which))[t];
         } else if (slots[u] != -1 && e0 == 0) {
@@ -149,18 +151,26 @@ __global__ void __launch_bounds__(kThreads) read_rows(const Rows p) {
     for (int u = 0; u < U; ++u) {
         const int64_t token = k.token + u * kRows;
         if (token >= p.n) continue;
-        float v[8];
-        values<FMT>(c[u], FMT == QC_E2M1 ? e4m3_value(block[u]) : 0.f, v);
         const bool held = slots[u] >= 0 && slots[u] < p.slots_end;
+        const float sb = FMT == QC_E2M1 ? e4m3_value(block[u]) : 0.f;
+        T *to = out + (token * p.g.heads + k.h) * D + e0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = held ? v[i] * scale[u] : 0.f;
-        Eight<T>::store(out + (token * p.g.heads + k.h) * D + e0, v);
+        for (int half = 0; half < 2; ++half) {
+            float v[8];
+            if constexpr (FMT == QC_E2M1)
+                values<FMT>(make_uint2(half ? c[u].y : c[u].x, 0), sb, v);
+            else
+                values<FMT>(half ? make_uint2(c[u].z, c[u].w) : make_uint2(c[u].x, c[u].y), sb, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = held ? v[i] * scale[u] : 0.f;
+            Eight<T>::store(to + 8 * half, v);
+        }
     }
 }
 
 template <typename T, int D, int FMT, int U, bool WRITE>
 cudaError_t launch(const Rows &p, cudaStream_t s) {
-    constexpr int kPerBlock = kThreads / 32 * (32 / (D / 8)) * U;
+    constexpr int kPerBlock = kThreads / 32 * (32 / (D / (WRITE ? 8 : 16))) * U;
     const int64_t blocks = (p.n + kPerBlock - 1) / kPerBlock * p.g.heads;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)blocks, 2);
