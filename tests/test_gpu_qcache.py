@@ -167,6 +167,32 @@ def test_write_every_byte_and_read(fmt, kind, d, heads, page, n):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("kind", TYPES)
+def test_write_and_read_of_many_rows_at_any_allowed_alignment(fmt, kind):
+    d, heads, page, n = 128, 2, 64, 20011                       # enough for several rows to a lane group
+    dtype, _ = TYPES[kind]
+    ctx = context(fmt, d, heads, page)
+    n_pages = n // page + 2
+    r = np.random.default_rng(n)
+    slots = r.permutation(n_pages * page)[:n].astype(np.int64)
+    some = 16 // torch.empty((), dtype=dtype).element_size()    # 16 bytes: off the 32 of a whole store
+    x = rows((1, some + n * heads * d), 31, dtype)[0, some:].view(n, heads, d)
+    want = np.zeros((n_pages, oq.page_bytes(fmt, d, heads, page)), dtype=np.uint8)
+    pages = torch.from_numpy(want).cuda()
+    fq.qc_write(ctx, x, x, torch.from_numpy(slots).cuda(), pages)
+    xs = x.float().cpu().numpy()
+    oq.pack(want, slots, xs, xs, fmt, page)
+    np.testing.assert_array_equal(pages.cpu().numpy(), want)
+    held = torch.from_numpy(oq.values(*oq.quantise(xs, fmt), fmt).astype(np.float32)).to(dtype)
+    room = torch.full((2 * some + n * heads * d,), 3.0, dtype=dtype, device="cuda")
+    off, whole = room[some:-some].view(n, heads, d), torch.empty((n, heads, d), dtype=dtype, device="cuda")
+    assert off.data_ptr() % 32 == 16 and whole.data_ptr() % 32 == 0
+    fq.qc_read(ctx, pages, torch.from_numpy(slots).cuda(), off, whole)
+    assert torch.equal(off.cpu(), held) and torch.equal(whole.cpu(), held)
+    assert (room[:some] == 3).all() and (room[-some:] == 3).all() and fq.qc_status(ctx) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_write_edge_rows(fmt):
     ctx = context(fmt, 64, 1, 16)
     x = rows((12, 1, 64), 8, torch.float32)
