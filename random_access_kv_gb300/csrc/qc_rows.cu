@@ -7,8 +7,8 @@
 // magnitude is a butterfly over those lanes. A warp takes U rows per lane group, of consecutive tokens and one head
 // (which lie one after another in a page), all their loads under way together; neighbouring blocks take
 // neighbouring heads. 32,768 tokens of 8 heads of 128 (bf16, e2m1): written in 38 us (4.5 TB/s; bound by issue
-// slots, 83 %: the largest magnitude, exact products and conversions), read in 33 us (5.2 TB/s); a random read of 104,864 tokens (int8 to
-// fp16) in 103 us (6.3 TB/s).
+// slots, 83 %: the largest magnitude, exact products and conversions), read in 33 us (5.2 TB/s); a random read of
+// 104,864 tokens (int8 to fp16) in 103 us (6.3 TB/s).
 #include "qc_formats.cuh"
 
 namespace qc {
