@@ -117,6 +117,8 @@ int qc_read(qc_ctx *ctx, int type, int64_t n, const int64_t *slots, const void *
  *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(s_t - max s),  s_t = scale * q . k_t,
  *   lse = log sum_t exp(s_t),  t over the places seen.
  * A row that sees nothing, and every row of a node i >= nodes[b], has out = 0 and lse = -inf.
+ * A row that sees a place and whose query holds a NaN or an infinity, or a score above float32's range, has
+ * out = NaN and lse = NaN (scores below it weigh nothing).
  * n_nodes = 1 is the single-token step of a decoder.
  *   type      : QC_F16 or QC_BF16, of q and out.
  *   n_nodes   : 1 .. 1024 nodes per sequence, that of the longest.

@@ -78,12 +78,12 @@ __global__ void __launch_bounds__(kThreads) join_parts(const Attend p, const Par
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;      // a NaN goes out
     T *out = static_cast<T *>(p.out) + out_row * D + lane * (D / 32);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) o[i] *= inv;
     store_row<T, D / 32>(out, o);
-    if (p.lse && lane == 0) p.lse[out_row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && lane == 0) p.lse[out_row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 template <typename T, int D>

@@ -522,7 +522,7 @@ __device__ __forceinline__ void load_queries(const Attend &p, const Walk &w, int
                 e.get(f);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[8 * i + j] = f[j];
+            for (int j = 0; j < 8; ++j) v[8 * i + j] = finite_or_nan(f[j]);
         }
         float back = 1.f;
         if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const 
                 for (int i = 0; i < D / 16; ++i) v[2 * i] = z.o[n][i][e] * unit, v[2 * i + 1] = z.o[n][i][2 + e] * unit;
                 if (whole) {
                     const int node = rr / p.group, h = kv * p.group + rr % p.group;
-                    const bool there = node < w.n.y && l > 0.f;
+                    const bool there = node < w.n.y && l != 0.f;        // a NaN goes out
                     const float inv = there ? 1.f / l : 0.f;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) v[i] = there ? v[i] * inv : 0.f;

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                 const bool whole = run.from == 0 && run.end == w.tiles;
                 const int64_t part = 2 * (int64_t)blockIdx.x + (segment ? 1 : 0);
                 const float sum = l.x + l.y;
-                const bool some = sum > 0.f && node < w.n.y;
+                const bool some = sum != 0.f && node < w.n.y;        // a NaN goes out
                 // out = O / (unit) / (l / unit); a part keeps l and O free of the unit
                 const float unit = __uint_as_float((uint32_t)(127 - e) << 23);
                 const float by = whole ? (some ? 1.f / sum : 0.f) : unit;

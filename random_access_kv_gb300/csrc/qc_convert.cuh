@@ -19,6 +19,10 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+// x, or NaN for an infinity: of a query, whose product with a code may be a plain infinity or none, so that every
+// score of its row is a NaN.
+__device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
+
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

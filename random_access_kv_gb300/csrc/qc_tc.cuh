@@ -185,6 +185,8 @@ __device__ __forceinline__ float put_query(const T *q, bool there, unsigned char
             Eight<T> e;
             e.load(q + 8 * i);
             e.get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = finite_or_nan(v[j]);
         }
         *reinterpret_cast<uint4 *>(out + (i >> 3) * (chunk_rows * 128) + r * 128 + (((i & 7) ^ (r & 7)) * 16)) =
             make_uint4(pack2(v[0] * f, v[1] * f), pack2(v[2] * f, v[3] * f), pack2(v[4] * f, v[5] * f), pack2(v[6] * f, v[7] * f));
