@@ -19,10 +19,13 @@
 //
 // Arithmetic is that of qc_attend_rows.cuh: exact products of fp16 operands, float32 sums; weights relative to a
 // reference that is put 2^3 above a score that passes it, times the values' row scale, in fp16 (two of them for
-// fp16 outputs). Their unit is a power of two (2^12 over the bound of the values' scales) and is folded into the
-// exponent, so the running sum l is in that unit too. fp16 holds a weight to 11 bits down to 2^-14, that is 2^-23
-// of the heaviest or less: lighter ones are not followed further here, where prefixes are long. (A reference 2^9
-// above the score moves less often, 0.36 instead of 0.39 ms at 256 rows, and leaves 2^-17.)
+// fp16 outputs). The products' unit is a power of two of each row's own, folded into the exponent, so that the
+// running sum l is in it too. It starts at 2^12 over the first scales and follows the row's largest product, which it
+// keeps between 2^4 and fp16's largest, whatever the values of places that the row does not see or gives no weight. So
+// fp16's least step of 2^-24 is 2^-28 of the largest product or less; lighter ones are not followed further here,
+// where prefixes are long. (A reference 2^9 above the score moves less often, 0.36 instead of 0.39 ms at 256 rows,
+// and leaves 2^-22. One unit per warp from the scales' bound alone: 0.379 ms instead of 0.385, and rows lost whose
+// values were 2^-34 of the largest.)
 #include <math.h>
 
 #include "qc_attend.cuh"
@@ -37,8 +40,10 @@ using namespace fq::sm100;
 // the reference moved with the next half tile, which costs the sums' rescaling but no second sweep.
 constexpr float kLag = 3.9f, kSoon = 2.f;
 constexpr float kHead = 3.f;            // how far above the largest score a new reference is put
-constexpr int kTop = 12;                // weights' unit: 2^12 over the scales' bound
-constexpr int kMostRaw = 8;
+// A row's unit 2^e is such that its largest product of a weight and its value's scale lies between 2^kFaint and 2^kMost.
+constexpr int kTop = 12;                // a new unit brings the scales, or the largest product, up to 2^kTop
+constexpr int kMostUnit = 100;          // sums of weights in the unit stay in float32
+constexpr float kFaint = 4.f, kMost = 15.95f;
 
 template <int D>
 constexpr int kOperand = kTile * D * 2;     // bytes of one fp16 operand tile
@@ -52,10 +57,16 @@ struct Small {
     Bars b;
     alignas(16) float ks[4][kTile], vs[4][kTile];       // scales of a tile's places (keys': times scale * log2 e)
     alignas(16) uint32_t exist[4][4];                   // places that exist
-    alignas(16) float vtop[4][4];                       // largest values' scale of each quarter
+    alignas(16) float vtop[4][4], vleast[4][4];         // log2 of each quarter's largest and least values' scale
     Walk start;
     uint32_t tmem;
 };
+
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 
 struct Plan {
     int device;
@@ -148,8 +159,13 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         const float vs = good ? scale[kTile] : 0.f;
                         sm.ks[it & 3][t] = good ? scale[0] * up : 0.f;
                         sm.vs[it & 3][t] = vs;
-                        const uint32_t e = __ballot_sync(0xffffffffu, good), m = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
-                        if (lane == 0) sm.exist[it & 3][quarter] = e, sm.vtop[it & 3][quarter] = __uint_as_float(m);
+                        const uint32_t e = __ballot_sync(0xffffffffu, good), bits = __float_as_uint(vs);
+                        const uint32_t most = __reduce_max_sync(0xffffffffu, bits), least = __reduce_min_sync(0xffffffffu, bits);
+                        if (lane == 0) {
+                            sm.exist[it & 3][quarter] = e;
+                            sm.vtop[it & 3][quarter] = lg2(__uint_as_float(most));
+                            sm.vleast[it & 3][quarter] = lg2(__uint_as_float(least));
+                        }
                     }
                     unsigned char *out = which == 0 ? k_op : v_op + (it & 1) * kOp;
                     convert_row<FMT, D>(st, st + I::kBlockScales + t * I::kBlocks, t, short_runs, good,
@@ -234,8 +250,9 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.q_ready);
             const uint32_t *tree = p.tree ? p.tree + ((int64_t)w.b * p.n_nodes + node) * p.words : nullptr;
-            float m = -INFINITY, ref = 0.f;
+            float m = -INFINITY;
             int e = 0;                          // log2 of the weights' unit
+            float big = -INFINITY;              // log2 of the row's largest product so far, or less, in the unit
             float2 l = make_float2(0.f, 0.f);
             float soon = -INFINITY;             // the row's next reference, where one waits
             for (int tile = run.from; ok && tile < run.end; ++tile, ++it) {
@@ -248,12 +265,14 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         const float4 vt = *reinterpret_cast<const float4 *>(sm.vtop[it & 3]);
                         const uint2 ex = *reinterpret_cast<const uint2 *>(&sm.exist[it & 3][2 * half]);
                         const bool mask = place + 64 > w.n.x || (ex.x & ex.y) != 0xffffffffu;
-                        const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w);
+                        const float4 vl = *reinterpret_cast<const float4 *>(sm.vleast[it & 3]);
+                        const float vtop = fmaxf(fmax3(vt.x, vt.y, vt.z), vt.w), vleast = fminf(fminf(vl.x, vl.y), fminf(vl.z, vl.w));
                         const uint32_t s_at = tmem + lanes + buf * 64;
                         uint32_t pw[32 * kTerms];
                         float2 sum;
                         float top;
-                        // one pass with the reference as it is; a second if a score or a scale has passed it too far
+                        // one pass with the reference and the unit as they are; others if a score or a product is too
+                        // far from them
                         auto sweep = [&](auto masked) {
                             constexpr bool kMasked = decltype(masked)::value;
                             const float mm = (m == -INFINITY ? 0.f : m) - (float)e;
@@ -327,22 +346,51 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         if (moved) {
                             const float m2 = fmaxf(soon, m);
                             by = m2 == m ? 1.f : ex2(m - m2);
+                            big -= m2 == m ? 0.f : m2 - m;
                             m = m2;
                         }
+                        // The row's largest product lies between the heaviest place's weight times the tile's least
+                        // scale (where nothing is masked) and times its largest: scores within `lower` and `upper` need
+                        // no more, reference and unit serve. Others have the products looked at.
                         for (int pass = 0;; ++pass) {
+                            const bool none = m == -INFINITY;
+                            const float at = m - (float)e, upper = fminf(m + kLag, at + kMost - vtop);
+                            float lower = mask ? INFINITY : at + kFaint - vleast;
+                            if (none || big >= kFaint || vtop == -INFINITY) lower = -INFINITY;
                             if (mask)
                                 sweep(std::true_type{});
                             else
                                 sweep(std::false_type{});
                             top *= down;
-                            if (pass || !__any_sync(0xffffffffu, top > m + kLag || vtop > ref)) break;
-                            const float m2 = top > m + kLag ? top + kHead : m;
-                            const float ref2 = fmaxf(ref, fmaxf(power_above(vtop), 3.2311742677852644e-27f));     // at least 2^-88
-                            const int e2 = kTop + 127 - (int)(__float_as_uint(ref2) >> 23);
-                            by = m == -INFINITY ? 0.f : by * ex2(m - m2 + (float)(e2 - e));
-                            moved = true;
+                            if (pass == 12 || !__any_sync(0xffffffffu, top > upper || top < lower)) {
+                                if (!mask) big = fmaxf(big, top - at + vleast);
+                                break;
+                            }
+                            uint32_t t[2] = {pw[0], pw[1]};
+#pragma unroll
+                            for (int i = 2; i < 32; ++i) t[i & 1] = max2(t[i & 1], pw[i]);
+                            const float2 f2 = float2_of(max2(t[0], t[1]));
+                            const bool lag = top > m + kLag;
+                            float high = big;
+                            bool off = false;
+                            if (!lag && !none && vtop > -INFINITY) {
+                                high = fmaxf(big, lg2(fmaxf(f2.x, f2.y)));
+                                off = high > kMost || (high < kFaint && e < kMostUnit && fabsf(top) < INFINITY);
+                            }
+                            if (high <= kMost) big = high;
+                            if (!__any_sync(0xffffffffu, lag || off)) break;
+                            const float m2 = lag ? top + kHead : m;
+                            int e2 = e;
+                            if (none && lag)
+                                e2 = vtop > -INFINITY ? min(kTop - (int)ceilf(vtop), kMostUnit) : e;
+                            else if (off)       // products beyond fp16's range: a step on
+                                e2 = high > kMost ? max(e - 36, min(kTop - (int)ceilf(vtop), kMostUnit))
+                                                  : min(e + (high > -INFINITY ? min(kTop - (int)floorf(high), 100) : 36), kMostUnit);
+                            moved |= __any_sync(0xffffffffu, m2 != m || e2 != e);
+                            const float d = none ? -INFINITY : m - m2 + (float)(e2 - e);
+                            by *= ex2(d);
+                            big += d;
                             m = m2;
-                            ref = ref2;
                             e = e2;
                         }
                         if (moved) {

@@ -39,6 +39,11 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 // Two e4m3 codes (low half of x) as fp16.
 __device__ __forceinline__ uint32_t cvt_e4m3(uint32_t x) {
     uint32_t r;

@@ -1,0 +1,95 @@
+"""Values of unlike magnitude in one sequence, in the paged cache's attention: what a row sees is held to the bound of
+its own largest product of weight and value scale, however large the values of places are that it does not see or
+gives no weight; and elements that are zero in every heavy place."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from random_access_kv_gb300 import build as fbuild  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    fbuild.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+SIZES = [(10, 4), (34, 2)]                  # nodes and group: 40 and 68 rows, for the tensor-core kernel
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "e2m1"])
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("t,group", SIZES)
+@pytest.mark.parametrize("spread", [2.0 ** 12, 2.0 ** 30, 2.0 ** 40, 2.0 ** 90])
+def test_large_values_of_places_that_rows_do_not_see(fmt, kind, t, group, spread):
+    import qcache_cases as qc
+    lens = [1201, 50]
+    K = [qc.rows((n + t, 1, 64), 1) for n in lens]
+    V = [qc.rows((n + t, 1, 64), 2) * 2.0 ** -3 for n in lens]
+    for v, n in zip(V, lens):
+        v[n] *= spread                       # the first node: seen by itself only
+    sees = np.broadcast_to(np.eye(t, dtype=bool), (2, t, t)).copy()
+    case = qc.Case(fmt, 64, 1, 32, K, V, lens, None, t, 1201)
+    q = qc.rows((2, t, group, 64), 3, qc.TYPES[kind][0])
+    out, lse = case.call(q, sees)
+    skip = {(0, 0), (1, 0)} if kind == "fp16" else ()       # their own values are beyond fp16
+    case.check(q, out, lse, sees, skip=skip)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e2m1"])
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("t,group", SIZES)
+@pytest.mark.parametrize("where", ["first", "middle", "last", "all over"])
+@pytest.mark.parametrize("bits", [24, 34, 45])
+def test_large_values_that_have_no_weight(fmt, kind, t, group, where, bits):
+    """Places of weight exp(-60) or so have values 2^bits times the others'."""
+    import qcache_cases as qc
+    n = 1301
+    k, v = qc.rows((n + t, 1, 64), 4) * 0.3, qc.rows((n + t, 1, 64), 5) * 2.0 ** -8
+    far = {"first": [0, 1], "middle": [640, 700], "last": [n - 1], "all over": list(range(5, n, 97))}[where]
+    k[..., 0] = 10.0
+    k[far, :, 0] = -50.0
+    v[far] *= 2.0 ** bits
+    case = qc.Case(fmt, 64, 1, 64, [k], [v], [n], None, t)
+    q = qc.rows((1, t, group, 64), 6, qc.TYPES[kind][0]) * 0.5
+    q[..., 0] = 8.0
+    out, lse = case.call(q)
+    case.check(q, out, lse)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("t,group", SIZES)
+@pytest.mark.parametrize("bits", [10, 30, 60])
+def test_the_heaviest_place_holds_least(kind, t, group, bits):
+    """Scores rise along the prefix in steps and values fall, so that references and units move apart."""
+    import qcache_cases as qc
+    n = 2000
+    step = torch.arange(n + t, device="cuda") // 100
+    k, v = qc.rows((n + t, 1, 64), 7) * 0.2, qc.rows((n + t, 1, 64), 8)
+    k[..., 0] = (step.float() * 5)[:, None]
+    v *= torch.exp2(-step.float() * bits / 20)[:, None, None]
+    case = qc.Case("int8", 64, 1, 16, [k], [v], [n], None, t)
+    q = qc.rows((1, t, group, 64), 9, qc.TYPES[kind][0]) * 0.5
+    q[..., 0] = 8.0
+    out, lse = case.call(q)
+    case.check(q, out, lse)
+
+
+@pytest.mark.parametrize("t,group", SIZES)
+@pytest.mark.parametrize("fmt", ["int8", "e2m1"])
+def test_an_element_that_is_zero_in_the_heavy_places(fmt, t, group):
+    """The bound that the header states holds for it: lighter weights may be off by 2^-29 of the heaviest product."""
+    import qcache_cases as qc
+    n = 1500
+    k, v = qc.rows((n + t, 1, 64), 10) * 0.2, qc.rows((n + t, 1, 64), 11)
+    k[..., 0] = 0.0
+    k[::50, :, 0] = 12.0
+    v[::50, :, 7] = 0.0
+    case = qc.Case(fmt, 64, 1, 16, [k], [v], [n], None, t)
+    for scale in (0.125, 0.5, 1.0, 1.5):
+        q = qc.rows((1, t, group, 64), 12, torch.bfloat16) * 0.2
+        q[..., 0] = 1.5
+        out, lse = case.call(q, scale=scale)
+        case.check(q, out, lse, scale=scale)
