@@ -22,7 +22,9 @@
 // running bound of the scales seen. A row's reference m moves only when a score passes it by 3 (base 2), to 3
 // above that score: so p_t <= 2^3 and w_t <= 2^15, the sums are rescaled seldom (a first tile's reference
 // serves until a score is 2^6 times heavier), and the maximum is only reduced over the lanes when it is. w_t
-// keeps fp16's 11 bits down to 2^-14; `add_tile` says what becomes of lighter weights, and of the other bits.
+// keeps fp16's 11 bits down to 2^-14; `add_tile` says what becomes of lighter weights, and of the other bits. A query
+// whose sums turn out below kLeastSum of what the unit is for (all values that it gives weight are small beside
+// others of the sequence) has the segment's places taken again in float32, one after the other (`plain_rows`).
 //
 // Order of elements. A sum over d may take them in any order as long as both operands do: lane c of a quad
 // takes elements c d / 4 .. of a key, so one 16-byte load feeds four (e2m1: eight) steps. For the values lane
@@ -52,6 +54,7 @@ constexpr float kHead = 3.f;            // how far above the largest score a new
 constexpr float kLeastNormal = 6.103515625e-05f;    // 2^-14, fp16's
 constexpr float kLift = 16777216.f;     // 2^24
 constexpr float kHeavy = 2.44140625e-04f;   // 2^-12
+constexpr float kLeastSum = 0.03125f;       // 2^-5: fp16's least step is 2^-19 of it
 // Heavy places that a row must have met: so many that no element is zero in all of them. About one in six
 // e2m1 codes is a zero, one in fifty of int8's, one in thousands of e4m3's.
 template <int FMT>
@@ -583,8 +586,84 @@ __device__ __forceinline__ Seen<NT> look(const Attend &p, const Walk &w, int t0,
     return seen;
 }
 
+// Places first .. last - 1 of one query row in float32, one after the other (the whole warp; a lane holds D / 32
+// elements). m, l and o as add_tile leaves them.
+template <typename T, int FMT, int D>
+__device__ __forceinline__ void plain_row(const Attend &p, int b, int2 n, int kv, int row, int first, int last, int lane, float &m, float &l,
+                                          float (&o)[D / 32]) {
+    using S = Shape<FMT, D>;
+    constexpr int E = D / 32;
+    const int node = row / p.group, h = kv * p.group + row % p.group;
+    const T *q = static_cast<const T *>(p.q) + b * p.q_seq + node * p.q_node + h * p.q_head + lane * E;
+    const uint32_t *tree = p.tree ? p.tree + ((int64_t)b * p.n_nodes + node) * p.words : nullptr;
+    const int32_t *table = p.table + b * p.table_stride;
+    float x[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = (float)q[i], o[i] = 0.f;
+    m = -INFINITY, l = 0.f;
+    // the lane's E elements of place t's keys or values, scaled
+    auto fetch_row = [&](const unsigned char *part, int which, int t, float (&v)[E]) {
+        const int byte = t * S::kRow + lane * S::kRow / 32;
+        const unsigned char *c = part + p.g.codes(which) + piece_at(byte >> 4) * 16 + (byte & 15);
+        const float scale = reinterpret_cast<const float *>(part + p.g.scales(which))[t];
+        float block = 0.f;
+        if constexpr (FMT == QC_E2M1) block = e4m3_value(part[p.g.block_scales(which) + t * S::kBlocks + lane * E / 16]) * 16384.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if constexpr (FMT == QC_INT8) v[i] = (float)(signed char)c[i] * scale;
+            if constexpr (FMT == QC_E4M3) v[i] = e4m3_value(c[i]) * scale;
+            if constexpr (FMT == QC_E2M1) v[i] = float2_of(half2_e2m1((c[i / 2] >> (4 * (i & 1))) & 0xfu)).x * block * scale;
+        }
+    };
+    for (int t = first; t < last; ++t) {
+        if (t >= n.x && !(window(p, tree, node, n.y, t - n.x) & 1u)) continue;
+        const int page = __ldg(table + (t >> p.g.shift));
+        if (page < 0 || page >= p.n_pages) continue;
+        const unsigned char *part = p.pages + ((int64_t)page * p.g.heads + kv) * (int64_t)p.g.part;
+        float v[E], s = 0.f;
+        fetch_row(part, 0, t & (p.g.page - 1), v);
+#pragma unroll
+        for (int i = 0; i < E; ++i) s = fmaf(x[i], v[i], s);
+#pragma unroll
+        for (int i = 16; i >= 1; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+        s *= p.scale * kLog2e;
+        const float top = fmaxf(m, s), old = m == -INFINITY ? 0.f : exp2f(m - top), weight = exp2f(s - top);
+        fetch_row(part, 1, t & (p.g.page - 1), v);
+        l = fmaf(l, old, weight);
+#pragma unroll
+        for (int i = 0; i < E; ++i) o[i] = fmaf(v[i], weight, o[i] * old);
+        m = top;
+    }
+}
+
+// The rows of `faint` (bit r: row r0 + r) of a segment, anew and over what is there (the whole warp). Not inlined: it
+// is hardly ever called, and the tiles' loop needs the registers and the instruction cache.
+template <typename T, int FMT, int D>
+__device__ __noinline__ void plain_rows(const Attend &p, const Parts &parts, int b, int2 n, int kv, int r0, uint32_t faint, int first, int last,
+                                        int64_t part) {
+    const int lane = threadIdx.x & 31;
+    for (; faint; faint &= faint - 1) {
+        const int at_row = __ffs(faint) - 1, row = r0 + at_row, node = row / p.group, h = kv * p.group + row % p.group;
+        float m, l, v[D / 32];
+        plain_row<T, FMT, D>(p, b, n, kv, row, first, last, lane, m, l, v);
+        if (part < 0) {
+            const float inv = 1.f / l;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) v[i] *= inv;
+            const int64_t o = ((int64_t)b * p.n_nodes + node) * p.n_q_heads + h;
+            store_row<T, D / 32>(static_cast<T *>(p.out) + o * D + lane * (D / 32), v);
+            if (p.lse && lane == 0) p.lse[o] = (m + log2f(l)) * kLn2;
+        } else {
+            float *to = parts.row(part, at_row) + lane * (D / 32);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) to[i] = v[i];
+            if (lane == 0) *parts.stat(part, at_row) = make_float2(m, l);
+        }
+    }
+}
+
 template <typename T, int FMT, int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const Attend p, const Parts parts, const Plan plan) {
+__global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const __grid_constant__ Attend p, const __grid_constant__ Parts parts, const Plan plan) {
     using S = Shape<FMT, D>;
     constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 1;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -663,13 +742,22 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const 
         // part 2 c: the job that the warp's run begins with; 2 c + 1: the one it ends with
         const int64_t part = 2 * (int64_t)unit + (segment ? 1 : 0);
         const int g = lane >> 2, c = lane & 3;
+        uint32_t faint = 0;         // queries whose sums are too small for the unit: bit 2 n + e
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float l = column_sum(z.l[n][e]);
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) most = fmax3(most, fabsf(z.o[n][i][e]), fabsf(z.o[n][i][2 + e]));
+                const bool enough = (__ballot_sync(0xffffffffu, most >= kLeastSum * kTop<FMT>) >> c) & 0x11111111u;
                 const int at_row = 8 * n + 2 * c + e, rr = r0 + at_row;
                 if (rr >= R) continue;
+                if (!enough && z.ref > 0.f && l > 0.f && rr / p.group < w.n.y) {
+                    faint |= 1u << (2 * n + e);
+                    continue;
+                }
                 // the lane's elements g D / 8 ..
                 float v[D / 8];
                 const float unit = z.ref * (1.f / kWeight);
@@ -691,6 +779,17 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const 
                     if (g == 0) *parts.stat(part, at_row) = make_float2(z.m[n][e], l);
                 }
             }
+        }
+        // what they see is small beside other values of the sequence, of which the unit is
+        if (__any_sync(0xffffffffu, faint)) {
+            uint32_t rows = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t x = __shfl_sync(0xffffffffu, faint, i);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) rows |= ((x >> (2 * n)) & 3u) << (8 * n + 2 * i);
+            }
+            plain_rows<T, FMT, D>(p, parts, w.b, w.n, kv, r0, rows, from * kTile, min(end * kTile, w.n.x + w.n.y), whole ? -1 : part);
         }
         ++segment;
         w.left -= end - from;

@@ -16,7 +16,11 @@ def _built():
     assert torch.cuda.is_available(), "GPU tests need a CUDA device"
 
 
-SIZES = [(10, 4), (34, 2)]                  # nodes and group: 40 and 68 rows, for the tensor-core kernel
+SIZES = [(2, 2), (10, 4), (34, 2)]          # nodes and group: few rows; 40 and 68, for the tensor-core kernel
+
+
+def floor(t, group):
+    return 2.0 ** -20 if t * group <= 32 else None
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3", "e2m1"])
@@ -35,7 +39,7 @@ def test_large_values_of_places_that_rows_do_not_see(fmt, kind, t, group, spread
     q = qc.rows((2, t, group, 64), 3, qc.TYPES[kind][0])
     out, lse = case.call(q, sees)
     skip = {(0, 0), (1, 0)} if kind == "fp16" else ()       # their own values are beyond fp16
-    case.check(q, out, lse, sees, skip=skip)
+    case.check(q, out, lse, sees, skip=skip, floor=floor(t, group))
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e2m1"])
@@ -56,7 +60,7 @@ def test_large_values_that_have_no_weight(fmt, kind, t, group, where, bits):
     q = qc.rows((1, t, group, 64), 6, qc.TYPES[kind][0]) * 0.5
     q[..., 0] = 8.0
     out, lse = case.call(q)
-    case.check(q, out, lse)
+    case.check(q, out, lse, floor=floor(t, group))
 
 
 @pytest.mark.parametrize("kind", ["fp16", "bf16"])
@@ -74,7 +78,7 @@ def test_the_heaviest_place_holds_least(kind, t, group, bits):
     q = qc.rows((1, t, group, 64), 9, qc.TYPES[kind][0]) * 0.5
     q[..., 0] = 8.0
     out, lse = case.call(q)
-    case.check(q, out, lse)
+    case.check(q, out, lse, floor=floor(t, group))
 
 
 @pytest.mark.parametrize("t,group", SIZES)
@@ -92,4 +96,4 @@ def test_an_element_that_is_zero_in_the_heavy_places(fmt, t, group):
         q = qc.rows((1, t, group, 64), 12, torch.bfloat16) * 0.2
         q[..., 0] = 1.5
         out, lse = case.call(q, scale=scale)
-        case.check(q, out, lse, scale=scale)
+        case.check(q, out, lse, scale=scale, floor=floor(t, group))
