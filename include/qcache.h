@@ -149,7 +149,8 @@ int qc_attend(qc_ctx *ctx, int type, int64_t n_seq, int n_nodes, int n_q_heads, 
               const int32_t *nodes, const uint32_t *tree, const void *pages, int64_t n_pages, float scale,
               int64_t max_len, void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Bytes of workspace that qc_attend wants for these sizes; -1 on bad arguments. */
+/* Bytes of workspace that qc_attend wants for these sizes: enough for calls with fewer of each, too. -1 on bad
+ * arguments. */
 int64_t qc_attend_workspace(const qc_ctx *ctx, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len);
 
 /* qc_status - reads and clears the context's sticky QC_FLAG_* bits in one atomic exchange on the device

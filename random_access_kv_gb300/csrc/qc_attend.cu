@@ -124,11 +124,13 @@ bool many_rows(int64_t max_len, int n_nodes, int rows) { return rows > 32 && max
 
 }  // namespace
 
+// Of these sizes and of all smaller ones, whichever kernel they go to.
 int64_t attend_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {
     const int rows = n_nodes * (n_q_heads / c->heads);
     if (n_seq == 0) return 0;
-    if (many_rows(max_len, n_nodes, rows)) return tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len);
-    return c->d == 64 ? rows_workspace_d<64>(c, rows, n_seq, n_nodes, max_len) : rows_workspace_d<128>(c, rows, n_seq, n_nodes, max_len);
+    const int64_t few = c->d == 64 ? rows_workspace_d<64>(c, rows, n_seq, n_nodes, max_len) : rows_workspace_d<128>(c, rows, n_seq, n_nodes, max_len);
+    const int64_t many = many_rows(max_len, n_nodes, rows) ? tc_workspace(c, n_seq, n_nodes, n_q_heads, max_len) : 0;
+    return few > many ? few : many;
 }
 
 cudaError_t launch_attend(const qc_ctx *c, int type, const Attend &p, cudaStream_t s) {

@@ -798,29 +798,29 @@ __global__ void __launch_bounds__(32 * kWarps, per_sm(NT, D)) attend_rows(const 
     griddep_launch_dependents();
 }
 
+// Rows of a warp at most: 32, in eights (24 with heads of 128, whose fourth tile does not fit the registers).
+template <int D>
+constexpr int kMostRows = D == 64 ? 32 : 24;
+
+inline int units_rows(const qc_ctx *c, int nt, int d, int row_tiles, int64_t n_seq, int64_t places) {
+    const int units = per_sm(nt, d) * kWarps * c->num_sms;
+    const int64_t most = n_seq * c->heads * row_tiles * ((places + kTile - 1) / kTile);
+    return units > most ? (int)(most + kWarps - 1) / kWarps * kWarps : units;
+}
+
 template <int FMT, int D>
 Plan plan_rows(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
     using S = Shape<FMT, D>;
     Plan p;
     p.device = c->device;
-    // Up to 32 rows in a warp, in eights (24 with heads of 128, whose fourth tile does not fit the registers);
-    // more are dealt evenly to several, each with its own conversion.
-    constexpr int kMost = D == 64 ? 32 : 24;
-    p.row_tiles = (rows + kMost - 1) / kMost;
+    // more rows than kMostRows are dealt evenly to several warps, each with its own conversion
+    p.row_tiles = (rows + kMostRows<D> - 1) / kMostRows<D>;
     p.nt = ((rows + p.row_tiles - 1) / p.row_tiles + 7) / 8;
     p.stages = room(p.nt, D) / S::kStage;
     if (p.stages > 4) p.stages = 4;
     p.smem = p.stages * S::kStage;
-    p.units = per_sm(p.nt, D) * kWarps * c->num_sms;
-    const int64_t most = n_seq * c->heads * p.row_tiles * ((max_len + n_nodes + kTile - 1) / kTile);
-    if (p.units > most) p.units = (int)(most + kWarps - 1) / kWarps * kWarps;
+    p.units = units_rows(c, p.nt, D, p.row_tiles, n_seq, max_len + n_nodes);
     return p;
-}
-
-template <int FMT, int D>
-int64_t workspace(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
-    const Plan p = plan_rows<FMT, D>(c, rows, n_seq, max_len, n_nodes);
-    return workspace_bytes(n_seq, 2 * (int64_t)p.units, p.nt * 8, D);
 }
 
 template <typename T, int FMT, int D, int NT>
@@ -868,12 +868,17 @@ cudaError_t attend_rows_d<QC_ROWS_D>(const qc_ctx *c, int type, const Attend &p,
                                : pick<__nv_bfloat16, QC_E2M1, D>(c, type, p, s);
 }
 
+// The most that any call of up to these sizes wants: over all numbers of column tiles that up to so many rows take.
 template <>
 int64_t rows_workspace_d<QC_ROWS_D>(const qc_ctx *c, int rows, int64_t n_seq, int n_nodes, int64_t max_len) {
     constexpr int D = QC_ROWS_D;
-    return c->fmt == QC_INT8   ? workspace<QC_INT8, D>(c, rows, n_seq, max_len, n_nodes)
-           : c->fmt == QC_E4M3 ? workspace<QC_E4M3, D>(c, rows, n_seq, max_len, n_nodes)
-                               : workspace<QC_E2M1, D>(c, rows, n_seq, max_len, n_nodes);
+    int64_t most = 0;
+    for (int nt = 1; nt <= kMostRows<D> / 8 && 8 * (nt - 1) < rows; ++nt) {
+        const int units = units_rows(c, nt, D, (rows + kMostRows<D> - 1) / kMostRows<D>, n_seq, max_len + n_nodes);
+        const int64_t bytes = workspace_bytes(n_seq, 2 * (int64_t)units, nt * 8, D);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 }  // namespace qc

@@ -458,6 +458,11 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
     if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
+int units_tc(const qc_ctx *c, int row_tiles, int64_t n_seq, int64_t places) {
+    const int64_t most = n_seq * c->heads * row_tiles * ((places + kTile - 1) / kTile);
+    return c->num_sms > most ? (int)most : c->num_sms;
+}
+
 template <int FMT, int D>
 Plan plan_tc(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
     using I = Item<FMT, D>;
@@ -469,16 +474,8 @@ Plan plan_tc(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_no
     p.raw = (227 * 1024 - fixed) / I::kBytes;
     if (p.raw > kMostRaw) p.raw = kMostRaw;
     p.smem = fixed + p.raw * I::kBytes;
-    p.units = c->num_sms;
-    const int64_t most = n_seq * c->heads * p.row_tiles * ((max_len + n_nodes + kTile - 1) / kTile);
-    if (p.units > most) p.units = (int)most;
+    p.units = units_tc(c, p.row_tiles, n_seq, max_len + n_nodes);
     return p;
-}
-
-template <int FMT, int D>
-int64_t workspace(const qc_ctx *c, int rows, int64_t n_seq, int64_t max_len, int n_nodes) {
-    const Plan p = plan_tc<FMT, D>(c, rows, n_seq, max_len, n_nodes);
-    return workspace_bytes(n_seq, 2 * (int64_t)p.units, p.nm * 128, D);
 }
 
 template <typename T, int FMT, int D, int NM>
@@ -521,16 +518,13 @@ cudaError_t launch_attend_tc(const qc_ctx *c, int type, const Attend &p, cudaStr
                                : pick<QC_E2M1, 128>(c, type, p, s);
 }
 
+// The most that any call of up to these sizes wants: one row tile or two.
 int64_t tc_workspace(const qc_ctx *c, int64_t n_seq, int n_nodes, int n_q_heads, int64_t max_len) {
     const int rows = n_nodes * (n_q_heads / c->heads);
-    if (n_seq == 0) return 0;
-    if (c->d == 64)
-        return c->fmt == QC_INT8   ? workspace<QC_INT8, 64>(c, rows, n_seq, max_len, n_nodes)
-               : c->fmt == QC_E4M3 ? workspace<QC_E4M3, 64>(c, rows, n_seq, max_len, n_nodes)
-                                   : workspace<QC_E2M1, 64>(c, rows, n_seq, max_len, n_nodes);
-    return c->fmt == QC_INT8   ? workspace<QC_INT8, 128>(c, rows, n_seq, max_len, n_nodes)
-           : c->fmt == QC_E4M3 ? workspace<QC_E4M3, 128>(c, rows, n_seq, max_len, n_nodes)
-                               : workspace<QC_E2M1, 128>(c, rows, n_seq, max_len, n_nodes);
+    const int64_t one = workspace_bytes(n_seq, 2 * (int64_t)units_tc(c, 1, n_seq, max_len + n_nodes), 128, c->d);
+    if (rows <= 128) return one;
+    const int64_t two = workspace_bytes(n_seq, 2 * (int64_t)units_tc(c, (rows + 255) / 256, n_seq, max_len + n_nodes), 256, c->d);
+    return one > two ? one : two;
 }
 
 }  // namespace qc
