@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                 for (int which = 0; which < 2; ++which) {
                     // the operand's last reader, then the codes
                     if (which == 0) {
-                        if (it >= 1) ok = warp_wait(&bar.k_free, it - 1);
+                        if (it >= 1) ok = ok && warp_wait(&bar.k_free, it - 1);
                     } else {
-                        if (it >= 2) ok = warp_wait(&bar.v_free[it & 1], (it >> 1) - 1);
+                        if (it >= 2) ok = ok && warp_wait(&bar.v_free[it & 1], (it >> 1) - 1);
                     }
                     ok = ok && warp_wait(&bar.raw.full[stage], phase);
                     if (!ok) break;
@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             }
             // products under way end before the operands' shared memory and the TMEM go
             mma_commit(&bar.last);
-            ok = mbar_wait(&bar.last, 0) && ok;
+            const bool ended = mbar_wait(&bar.last, 0);      // also where a wait gave up before
+            ok = ok && ended;
         }
         ok = __all_sync(0xffffffffu, ok);
     } else {
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
             for (int tile = run.from; ok && tile < run.end; ++tile, ++it) {
                 for (int half = 0; half < 2; ++half) {
                     const int buf = 2 * rt + half, place = tile * kTile + 64 * half;
-                    ok = warp_wait(&bar.s_full[buf], it);
+                    ok = ok && warp_wait(&bar.s_full[buf], it);
                     if (!ok) break;
                     if (active) {
                         tc_fence_after();
@@ -327,7 +328,8 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                         };
                         // the sums so far, in another unit
                         auto rescale = [&](float by) {
-                            ok = warp_wait(&bar.o_done[rt], 2 * it + half - 1);
+                            ok = ok && warp_wait(&bar.o_done[rt], 2 * it + half - 1);
+                            if (!ok) return;        // products may still be added to them
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                             l.x *= by;
                             l.y *= by;
                             if (sums) rescale(by);
+                            if (!ok) break;
                         }
                         soon = top > m + kSoon ? top + kHead : -INFINITY;
                         l = add2f(l, sum);
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                     if (lane == 0) mbar_arrive(&bar.p_ready[buf]);
                 }
             }
-            if (ok) ok = warp_wait(&bar.job_done, segment);
+            ok = ok && warp_wait(&bar.job_done, segment);
             if (!ok) break;
             if (active) {
                 tc_fence_after();

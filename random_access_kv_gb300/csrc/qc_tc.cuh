@@ -298,7 +298,7 @@ __device__ __forceinline__ bool produce(const Attend &p, Run &run, int jobs, int
             const uint32_t v_round = round;
             forward(2 * warps - 1);
             bool ok = true;
-            if (k_round) ok = warp_wait(&ring.empty[k], k_round - 1);
+            if (k_round) ok = ok && warp_wait(&ring.empty[k], k_round - 1);
             if (v_round) ok = ok && warp_wait(&ring.empty[v], v_round - 1);
             if (!ok) return false;
             unsigned char *kt = raw + k * I::kBytes, *vt = raw + v * I::kBytes;
