@@ -81,7 +81,7 @@ int64_t qc_page_bytes(const qc_ctx *ctx);
  *   rot         : rotated elements, a multiple of 16, 0 <= rot <= d. 0: the norm alone (pos and table
  *                 are not read).
  *   q_out, k_out: as q and k with strides of their own; they may be q and k themselves.
- * Every row starts on a 16-byte boundary (FQ_EALIGN). eps is finite and >= 0.
+ * Every row starts on a 16-byte boundary (FQ_EALIGN). eps is finite and >= 0, n <= 2^32.
  */
 int qc_norm_rope(qc_ctx *ctx, int type, int64_t n, const void *q, int hq, int64_t q_token, int64_t q_head,
                  const float *wq, const void *k, int hk, int64_t k_token, int64_t k_head, const float *wk, float eps,
@@ -95,6 +95,7 @@ int qc_norm_rope(qc_ctx *ctx, int type, int64_t n, const void *q, int hq, int64_
  *            [0, n_pages * page_tokens) skips it and sets QC_FLAG_RANGE.
  *   pages  : device bytes [n_pages][qc_page_bytes], 16-byte aligned. Bytes of other tokens are not
  *            written.
+ * n <= 2^32 and n * n_heads <= 2^35, here and in qc_read.
  */
 int qc_write(qc_ctx *ctx, int type, int64_t n, const void *k, int64_t k_token, int64_t k_head, const void *v,
              int64_t v_token, int64_t v_head, const int64_t *slots, void *pages, int64_t n_pages, void *stream);

@@ -48,7 +48,10 @@ int check_pages(const qc_ctx *ctx, const void *pages, int64_t n_pages) {
     return aligned(pages, 16) ? FQ_OK : FQ_EALIGN;
 }
 
-constexpr int64_t kMaxTokens = int64_t(1) << 40;
+// What the kernels' grids take.
+constexpr int64_t kMaxTokens = int64_t(1) << 32, kMaxRows = int64_t(1) << 35, kMaxPos = int64_t(1) << 40;
+
+bool too_many(const qc_ctx *ctx, int64_t n) { return n < 0 || n > kMaxTokens || n * ctx->heads > kMaxRows; }
 
 }  // namespace
 
@@ -101,7 +104,7 @@ int qc_norm_rope(qc_ctx *ctx, int type, int64_t n, const void *q, int hq, int64_
     if (!ctx || type < QC_F16 || type > QC_F32 || n < 0 || n > kMaxTokens) return FQ_EINVAL;
     if (hq < 0 || hk < 0 || hq > qc::kMaxHeads || hk > qc::kMaxHeads) return FQ_EINVAL;
     if (rot < 0 || rot > ctx->d || rot % 16 || !isfinite(eps) || eps < 0.f) return FQ_EINVAL;
-    if (rot > 0 && (max_pos < 0 || max_pos > kMaxTokens)) return FQ_EINVAL;
+    if (rot > 0 && (max_pos < 0 || max_pos > kMaxPos)) return FQ_EINVAL;
     if (n == 0 || hq + hk == 0) return FQ_OK;
     const int size = size_of(type);
     for (int i = 0; i < 4; ++i) {
@@ -134,7 +137,7 @@ int qc_norm_rope(qc_ctx *ctx, int type, int64_t n, const void *q, int hq, int64_
 
 int qc_write(qc_ctx *ctx, int type, int64_t n, const void *k, int64_t k_token, int64_t k_head, const void *v,
              int64_t v_token, int64_t v_head, const int64_t *slots, void *pages, int64_t n_pages, void *stream) {
-    if (!ctx || type < QC_F16 || type > QC_F32 || n < 0 || n > kMaxTokens) return FQ_EINVAL;
+    if (!ctx || type < QC_F16 || type > QC_F32 || too_many(ctx, n)) return FQ_EINVAL;
     int rc = check_pages(ctx, pages, n_pages);
     if (rc != FQ_OK) return rc;
     if (n == 0) return FQ_OK;
@@ -162,7 +165,7 @@ int qc_write(qc_ctx *ctx, int type, int64_t n, const void *k, int64_t k_token, i
 
 int qc_read(qc_ctx *ctx, int type, int64_t n, const int64_t *slots, const void *pages, int64_t n_pages, void *k_out,
             void *v_out, void *stream) {
-    if (!ctx || type < QC_F16 || type > QC_F32 || n < 0 || n > kMaxTokens) return FQ_EINVAL;
+    if (!ctx || type < QC_F16 || type > QC_F32 || too_many(ctx, n)) return FQ_EINVAL;
     const int rc = check_pages(ctx, pages, n_pages);
     if (rc != FQ_OK) return rc;
     if (n == 0 || (!k_out && !v_out)) return FQ_OK;
