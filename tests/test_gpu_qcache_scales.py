@@ -97,3 +97,30 @@ def test_an_element_that_is_zero_in_the_heavy_places(fmt, t, group):
         q[..., 0] = 1.5
         out, lse = case.call(q, scale=scale)
         case.check(q, out, lse, scale=scale, floor=floor(t, group))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "e2m1"])
+@pytest.mark.parametrize("scale", [0.75, 1.0, 1.25])
+def test_light_places_beside_settled_heavy_ones(fmt, scale):
+    """bf16 outputs of few rows: one channel is zero in all heavy places and large in the light ones, whose weights reach
+    below fp16's. What is lost is within 2^-20 of the row's largest element a light place, as the header states."""
+    import qcache_cases as qc
+    n, t, group = 900, 1, 4
+    k, v = torch.zeros((n + t, 1, 64), device="cuda"), qc.rows((n + t, 1, 64), 13)
+    k[:100, :, 0] = 12.0 + torch.rand(100, 1, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    k[100:, :, 0] = torch.linspace(-2.0, 2.0, n + t - 100, device="cuda")[:, None]
+    v[:100, :, 7], v[100:, :, 7] = 0.0, 100.0
+    case = qc.Case(fmt, 64, 1, 16, [k], [v], [n], None, t)
+    q = torch.zeros((1, t, group, 64), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 2.0
+    out, _ = case.call(q, scale=scale)
+    got = qc.host(out)[0, 0, 0]
+    s = 2 * scale * case.K[0][:, 0, 0]
+    p = np.exp(s - s.max())
+    p /= p.sum()
+    want, weight = p @ case.V[0][:, 0], p @ np.abs(case.V[0][:, 0])
+    e = 2 * scale * 72 * qc.U * np.abs(case.K[0][:, 0, 0]).max() + 4 * qc.U * np.abs(s).max()
+    tol = (2.0 ** -11 + 4 * e + 2.0 ** -20) * weight + qc.half_ulp(want, 8)
+    assert (np.abs(got - want) <= tol + (n + t) * 2.0 ** -20 * np.abs(want).max()).all()
+    others = np.arange(64) != 7
+    assert (np.abs(got - want) <= tol + (n + t) * 2.0 ** -34 * np.abs(want).max())[others].all()
