@@ -138,7 +138,8 @@ int qc_read(qc_ctx *ctx, int type, int64_t n, const int64_t *slots, const void *
  *               [n_seq][n_nodes][n_q_heads], or NULL.
  *   workspace : device, 16-byte aligned, at least qc_attend_workspace() bytes, used by one call at a
  *               time; its contents do not matter and mean nothing afterwards.
- * Products take the codes as they are, exactly; q is not rounded; sums are float32. The products p s of a weight and
+ * Products take the codes as they are, exactly, and q as it is, but for elements of a QC_BF16 row below 2^-30 of its
+ * largest, which are off by up to 2^-38 of that (float16's range); sums are float32. The products p s of a weight and
  * its value row's scale are rounded to 11 bits (one float16) for QC_BF16 and to 22 (two) for QC_F16. Above 32 query rows
  * (n_nodes * n_q_heads / n_heads) and from 1,024 places (max_len + n_nodes) on, those that are light beside the row's
  * largest are held to 2^-29 of it instead, so that an element which is zero wherever p s is large may lose that much

@@ -17,7 +17,8 @@
 // conversion, which costs most, goes over places, and few queries leave few columns empty. NT column tiles
 // of 8 queries share it. Codes are exact in fp16, and so are e2m1 codes times their e4m3 block scale (5
 // bits), so the products q . code are exact and summed in float32; the row's scale multiplies the score
-// afterwards. A bf16 query row is brought into fp16's range by a power of two (8 bits fit 11). For the values,
+// afterwards. A bf16 query row is brought into fp16's range by a power of two: 8 bits fit 11, and elements from 2^-30
+// of the row's largest on keep them all (below, fp16's step is 2^-37 of the largest). For the values,
 // the weight p_t times the row's scale is the operand: w_t = p_t * (s_t / ref) * 2^12, ref a power of two, the
 // running bound of the scales seen. A row's reference m moves only when a score passes it by 3 (base 2), to 3
 // above that score: so p_t <= 2^3 and w_t <= 2^15, the sums are rescaled seldom (a first tile's reference

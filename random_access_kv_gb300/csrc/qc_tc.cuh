@@ -173,7 +173,7 @@ __device__ __forceinline__ float put_query(const T *q, bool there, unsigned char
                 for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
             }
         }
-        // largest magnitude to [2^13, 2^14)
+        // largest magnitude to [2^13, 2^14): from 2^-17 on, 2^-30 of it, fp16 holds all 8 bits
         const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
         f = __uint_as_float((uint32_t)(13 - e + 127) << 23);
         down = __uint_as_float((uint32_t)(e - 13 + 127) << 23);

@@ -124,3 +124,23 @@ def test_light_places_beside_settled_heavy_ones(fmt, scale):
     assert (np.abs(got - want) <= tol + (n + t) * 2.0 ** -20 * np.abs(want).max()).all()
     others = np.arange(64) != 7
     assert (np.abs(got - want) <= tol + (n + t) * 2.0 ** -34 * np.abs(want).max())[others].all()
+
+
+@pytest.mark.parametrize("t,group", [(2, 2), (40, 1)])
+@pytest.mark.parametrize("low", [-28, -33, -36])
+def test_small_elements_of_a_bf16_query(t, group, low):
+    """Keys are zero where the query is largest: what counts is 2^low of it. Elements from 2^-30 on are exact, smaller
+    ones to a step of 2^-37 of the power of two below the largest, as the header states."""
+    import qcache_cases as qc
+    n = 1100
+    k = qc.rows((n + t, 1, 64), 14)
+    k[..., 0] = 0.0
+    case = qc.Case("int8", 64, 1, 16, [k], [qc.rows((n + t, 1, 64), 15)], [n], None, t)
+    q = (qc.rows((1, t, group, 64), 16) * 2.0 ** low).to(torch.bfloat16)
+    q[..., 0] = 1.5
+    out, lse = case.call(q, scale=2.0 ** -low / 8)
+    top = np.exp2(np.floor(np.log2(np.abs(qc.host(q)).max(-1, keepdims=True))))
+    held = np.rint(qc.host(q) / (top * 2.0 ** -37)) * (top * 2.0 ** -37)
+    if low == -28:
+        assert (np.abs(held - qc.host(q)) <= np.where(np.abs(qc.host(q)) < top * 2.0 ** -30, top * 2.0 ** -38, 0)).all()
+    case.check(torch.from_numpy(held).cuda(), out, lse, scale=2.0 ** -low / 8)
