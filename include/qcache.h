@@ -112,7 +112,7 @@ int qc_read(qc_ctx *ctx, int type, int64_t n, const int64_t *slots, const void *
 /*
  * qc_attend - softmax attention of the drafted tokens ("nodes") of n_seq sequences over the cache.
  * Sequence b holds lens[b] cached tokens, its prefix, at places 0 .. lens[b] - 1, and its node j at
- * place lens[b] + j (written there by qc_write); place t is slot
+ * place lens[b] + j (written there by qc_write, seen by others or not); place t is slot
  * table[b][t / page_tokens] * page_tokens + t % page_tokens. Node i < nodes[b] sees the whole prefix
  * and the nodes that its bits name. For query head h and the key/value head h / (n_q_heads / n_heads):
  *   out = sum_t p_t v_t / sum_t p_t,  p_t = exp(s_t - max s),  s_t = scale * q . k_t,

@@ -114,12 +114,14 @@ cudaError_t launch_join(const Attend &p, const Parts &parts, int type, int row_t
 namespace {
 
 // Which kernel. qc_attend_tc.cu pays 128 rows' tensor-core time and one thread's softmax per row whatever the
-// rows' number, qc_attend_rows.cuh its conversion and products anew for every 32 rows: the first is for more
-// than 32. Below about a thousand places a head's tiles of 128 are too few to hide its pipeline's start, and
-// rows whose weight lies on few places are likely, which qc_attend_rows.cuh follows to the last bit.
-//   e4m3, d = 64, 128 rows, 8 sequences of 4,096 places at most: 32 us here, 57 us there;
-//   int8, d = 128, 256 rows, 8 x 32,768: 0.38 ms and 1.6 ms; 20 rows, 16 x 16,384: 225 us and 167 us;
-//   e2m1, d = 128, 4 rows, 32 sequences of 32,768 at most: 0.49 ms and 0.17 ms (one-term weights).
+// rows' number, qc_attend_rows.cuh its conversion and products anew for every 24 or 32 rows: the first is for more
+// than 32. Below about a thousand places rows whose weight lies on few places are likely, and qc_attend_rows.cuh
+// follows their light weights further; that costs time where rows are many. Here (qc_attend_tc.cu) and there, us:
+//   int8, bf16, d = 128, 16 x 16,384, 20 rows: 283 and 178; 32: 289 and 246; 36: 290 and 344;
+//   the same in e2m1, 36 rows: 289 and 368; in fp16 queries, int8, 36 rows: 336 and 436;
+//   e4m3, fp16, d = 64, 8 sequences of 4,096 places at most, 32 rows: 41 and 40; 40: 30 and 35; 128: 38 and 101;
+//   e2m1, fp16, d = 128, 32 sequences of 32,768 places at most, 4 rows: 632 and 203; int8, bf16, 256 rows, 8 x 32,768:
+//   392 and 1,669; 256 rows, 8 x 960 places: 51 and 138 (below the rule's bound: the second runs).
 bool many_rows(int64_t max_len, int n_nodes, int rows) { return rows > 32 && max_len + n_nodes >= 1024; }
 
 }  // namespace

@@ -9,8 +9,8 @@
 //
 // What bounds it: in the limit the pages, read once; as measured the latency of dependent conversions and
 // products, two to three warps a scheduler. 4 rows over 32 sequences of up to 32,768 places (e2m1, fp16 queries, 637 MB)
-// take 182 us (3.5 TB/s, 52 % of the card's copy rate), 20 rows over 16 x 16,384 (int8, bf16 queries, 555 MB) 167
-// us (3.3 TB/s). With queries as the products' 16 rows and places as their 8 columns, twice the registers for the
+// take 186 us (3.4 TB/s, 50 % of the card's copy rate), 20 rows over 16 x 16,384 (int8, bf16 queries, 555 MB) 173
+// us (3.2 TB/s). With queries as the products' 16 rows and places as their 8 columns, twice the registers for the
 // outputs of up to 8 queries and eight warps on an SM, it was 226 and 195 us.
 //
 // Products. Places are the products' 16 rows and queries their 8 columns (S^T = K Q^T, O^T = V^T P^T): the
@@ -433,7 +433,7 @@ __device__ __forceinline__ void add_tile(const unsigned char *st, const Offsets<
     }
     // A weight to 11 bits, and for fp16 outputs what that leaves, to 22. With 11 an fp16 output was 1.3 to 1.7 times
     // as far from 64 bits as its own rounding is; bf16's eight bits hide it. (One token over 32 ragged sequences,
-    // e2m1: 170 us with one term, 182 with two.)
+    // e2m1: 170 us with one term, 182 with two, before rows were followed to their largest sums.)
     uint32_t p[TERMS][NT][2][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)

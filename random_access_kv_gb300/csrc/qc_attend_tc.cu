@@ -12,8 +12,8 @@
 // Scores and weights of a tile are two halves of 64 places, a buffer each: while a half's softmax runs, the
 // tensor cores take the other half's weights and make the next tile's scores.
 //
-// What bounds it: the softmax's and the conversion's issue slots and latency, with 256 rows 727 TFLOP/s of the
-// two products (38 % of a large matrix product's rate; 0.38 ms for 256 bf16 rows over 8 x 32,768 int8 places, 8
+// What bounds it: the softmax's and the conversion's issue slots and latency, with 256 rows 710 TFLOP/s of the
+// two products (37 % of a large matrix product's rate; 0.387 ms for 256 bf16 rows over 8 x 32,768 int8 places, 8
 // heads). A tile's half of 64 scores takes a softmax warp about 1,800 cycles, an operand's conversion a warp
 // about 1,300.
 //
@@ -23,9 +23,8 @@
 // running sum l is in it too. It starts at 2^12 over the first scales and follows the row's largest product, which it
 // keeps between 2^4 and fp16's largest, whatever the values of places that the row does not see or gives no weight. So
 // fp16's least step of 2^-24 is 2^-28 of the largest product or less; lighter ones are not followed further here,
-// where prefixes are long. (A reference 2^9 above the score moves less often, 0.36 instead of 0.39 ms at 256 rows,
-// and leaves 2^-22. One unit per warp from the scales' bound alone: 0.379 ms instead of 0.385, and rows lost whose
-// values were 2^-34 of the largest.)
+// where prefixes are long. (One unit per warp, from the scales' bound alone: 0.380 ms instead of 0.387, and rows lost
+// whose values were 2^-34 of the largest.)
 #include <math.h>
 
 #include "qc_attend.cuh"
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
     using I = Item<FMT, D>;
     // A weight to 11 bits, and for fp16 outputs what that leaves, to 22: with 11 an fp16 output was 1.5 to 1.7 times
     // as far from 64 bits as its own rounding is, bf16's eight bits hide it. (Trees of 16, e4m3: 31.5 us with one
-    // term, 35.3 with two.)
+    // term, 35.3 with two, 36 with units of the rows' own.)
     constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 1;
     constexpr int kOp = kOperand<D>, kSoft = 4 * NM, kConv = kSoft, kProducer = kSoft + 4, kMma = kProducer + kProducers;
     extern __shared__ __align__(1024) unsigned char smem[];
