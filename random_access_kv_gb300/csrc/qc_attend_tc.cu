@@ -19,11 +19,12 @@
 //
 // Arithmetic is that of qc_attend_rows.cuh: exact products of fp16 operands, float32 sums; weights relative to a
 // reference that is put 2^3 above a score that passes it, times the values' row scale, in fp16 (two of them for
-// fp16 outputs). The products' unit is a power of two of each row's own, folded into the exponent, so that the
-// running sum l is in it too. It starts at 2^12 over the first scales and follows the row's largest product, which it
-// keeps between 2^4 and fp16's largest, whatever the values of places that the row does not see or gives no weight. So
-// fp16's least step of 2^-24 is 2^-28 of the largest product or less; lighter ones are not followed further here,
-// where prefixes are long. (One unit per warp, from the scales' bound alone: 0.380 ms instead of 0.387, and rows lost
+// fp16 outputs). The values' scales of a job are multiplied by the power of two that brings those of its first tile
+// to 2^12. From there each row's products have a power of two of their own, folded into the exponent (the running
+// sum l is in it too; as a rule it is 1, so that weights keep their bits). It follows the row's largest product,
+// which it keeps between 2^4 and fp16's largest, whatever the values of places that the row does not see or gives no
+// weight. So fp16's least step of 2^-24 is 2^-28 of the largest product or less; lighter ones are not followed further
+// here, where prefixes are long. (One unit per warp, from the scales' bound alone: 0.380 ms instead of 0.387, and rows lost
 // whose values were 2^-34 of the largest.)
 #include <math.h>
 
@@ -42,6 +43,7 @@ constexpr float kHead = 3.f;            // how far above the largest score a new
 // A row's unit 2^e is such that its largest product of a weight and its value's scale lies between 2^kFaint and 2^kMost.
 constexpr int kTop = 12;                // a new unit brings the scales, or the largest product, up to 2^kTop
 constexpr int kMostUnit = 100;          // sums of weights in the unit stay in float32
+constexpr float kMostScale = 8.507059173023462e37f;     // 2^126
 constexpr float kFaint = 4.f, kMost = 15.95f;
 
 template <int D>
@@ -57,6 +59,7 @@ struct Small {
     alignas(16) float ks[4][kTile], vs[4][kTile];       // scales of a tile's places (keys': times scale * log2 e)
     alignas(16) uint32_t exist[4][4];                   // places that exist
     alignas(16) float vtop[4][4], vleast[4][4];         // log2 of each quarter's largest and least values' scale
+    float base[2];                                      // what a job's values' scales are multiplied by
     Walk start;
     uint32_t tmem;
 };
@@ -135,9 +138,10 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
         const int quarter = warp - kConv, t = quarter * 32 + lane;
         const bool short_runs = I::kRow == 32 && p.g.page == 16;
         const float up = p.scale * kLog2e;
-        int stage = 0;
+        int stage = 0, segment = 0;
         uint32_t phase = 0;
-        for (; ok && run.begin(); run.next(p, jobs, kTile)) {
+        float base = 1.f;
+        for (; ok && run.begin(); run.next(p, jobs, kTile), ++segment) {
             const int end = run.w.n.x + run.w.n.y;
             for (int tile = run.from; ok && tile < run.end; ++tile, ++it) {
 #pragma unroll 1
@@ -151,12 +155,20 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                     ok = ok && warp_wait(&bar.raw.full[stage], phase);
                     if (!ok) break;
                     const unsigned char *st = raw + stage * I::kBytes;
-                    const bool good = tile * kTile + t < end && !((bar.raw.bad[stage] >> (t >> 4)) & 1u);
+                    auto is_there = [&](int i) { return tile * kTile + i < end && !((bar.raw.bad[stage] >> (i >> 4)) & 1u); };
+                    const bool good = is_there(t);
                     if (which == 0) {
                         // the scales, the values' too: the softmax need not wait for the values
-                        const float *scale = reinterpret_cast<const float *>(st + I::kScales) + t;
-                        const float vs = good ? scale[kTile] : 0.f;
-                        sm.ks[it & 3][t] = good ? scale[0] * up : 0.f;
+                        const float *scale = reinterpret_cast<const float *>(st + I::kScales);
+                        if (tile == run.from) {     // the first tile's scales to 2^kTop, a power of two for the whole job
+                            float top = 0.f;
+                            for (int i = lane; i < kTile; i += 32) top = fmaxf(top, is_there(i) ? scale[kTile + i] : 0.f);
+                            const int x = (int)(__float_as_uint(power_above(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))))) >> 23);
+                            base = x ? __uint_as_float((uint32_t)min(max(127 + kTop + 127 - x, 27), 227) << 23) : 1.f;
+                            if (t == 0) sm.base[segment & 1] = base;
+                        }
+                        const float vs = good ? fminf(scale[kTile + t] * base, kMostScale) : 0.f;
+                        sm.ks[it & 3][t] = good ? scale[t] * up : 0.f;
                         sm.vs[it & 3][t] = vs;
                         const uint32_t e = __ballot_sync(0xffffffffu, good), bits = __float_as_uint(vs);
                         const uint32_t most = __reduce_max_sync(0xffffffffu, bits), least = __reduce_min_sync(0xffffffffu, bits);
@@ -376,7 +388,9 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                             bool off = false;
                             if (!lag && !none && vtop > -INFINITY) {
                                 high = fmaxf(big, lg2(fmaxf(f2.x, f2.y)));
-                                off = high > kMost || (high < kFaint && e < kMostUnit && fabsf(top) < INFINITY);
+                                // nothing to be seen even in the largest unit: back, where the sums of weights are best
+                                const bool blank = high == -INFINITY && pass >= 4;
+                                off = high > kMost || (blank ? e != 0 : high < kFaint && e < kMostUnit && fabsf(top) < INFINITY);
                             }
                             if (high <= kMost) big = high;
                             if (!__any_sync(0xffffffffu, lag || off)) break;
@@ -385,8 +399,10 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                             if (none && lag)
                                 e2 = vtop > -INFINITY ? min(kTop - (int)ceilf(vtop), kMostUnit) : e;
                             else if (off)       // products beyond fp16's range: a step on
-                                e2 = high > kMost ? max(e - 36, min(kTop - (int)ceilf(vtop), kMostUnit))
-                                                  : min(e + (high > -INFINITY ? min(kTop - (int)floorf(high), 100) : 36), kMostUnit);
+                                e2 = high > kMost       ? max(e - 36, min(kTop - (int)ceilf(vtop), kMostUnit))
+                                     : high > -INFINITY ? min(e + min(kTop - (int)floorf(high), 100), kMostUnit)
+                                     : pass < 4         ? min(e + 36, kMostUnit)
+                                                        : 0;
                             moved |= __any_sync(0xffffffffu, m2 != m || e2 != e);
                             const float d = none ? -INFINITY : m - m2 + (float)(e2 - e);
                             by *= ex2(d);
@@ -419,9 +435,9 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                 const int64_t part = 2 * (int64_t)blockIdx.x + (segment ? 1 : 0);
                 const float sum = l.x + l.y;
                 const bool some = sum != 0.f && node < w.n.y;        // a NaN goes out
-                // out = O / (unit) / (l / unit); a part keeps l and O free of the unit
+                // out = O / (unit base) / (l / unit); a part keeps l and O free of them
                 const float unit = __uint_as_float((uint32_t)(127 - e) << 23);
-                const float by = whole ? (some ? 1.f / sum : 0.f) : unit;
+                const float back = 1.f / sm.base[segment & 1], by = (whole ? (some ? 1.f / sum : 0.f) : unit) * back;
                 const int64_t at = ((int64_t)w.b * p.n_nodes + node) * p.n_q_heads + kv * p.group + h;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -445,7 +461,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
                     if (!whole)
                         *parts.stat(part, rt * 128 + r) = make_float2(m, sum * unit);
                     else if (p.lse)
-                        p.lse[at] = some ? (m + log2f(sum) - (float)e) * kLn2 : -INFINITY;
+                        p.lse[at] = some ? (m + log2f(sum * unit)) * kLn2 : -INFINITY;
                 }
                 tc_fence_before();
             }

@@ -144,3 +144,33 @@ def test_small_elements_of_a_bf16_query(t, group, low):
     if low == -28:
         assert (np.abs(held - qc.host(q)) <= np.where(np.abs(qc.host(q)) < top * 2.0 ** -30, top * 2.0 ** -38, 0)).all()
     case.check(torch.from_numpy(held).cuda(), out, lse, scale=2.0 ** -low / 8)
+
+
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+@pytest.mark.parametrize("t,group", SIZES)
+@pytest.mark.parametrize("size", [0, -80, 60])
+def test_log_sums_do_not_hang_on_the_values(kind, t, group, size):
+    """Rows that see zeros only, beside nodes that do not (0), and caches of very small and very large values: the
+    log-sum is as exact as that of any other."""
+    import qcache_cases as qc
+    lens = [5, 0, 1100]
+    K = [qc.rows((n + t, 1, 64), 17) * 0.1 for n in lens]
+    V = [qc.rows((n + t, 1, 64), 18) * 2.0 ** size for n in lens]
+    sees = np.broadcast_to(np.eye(t, dtype=bool), (3, t, t)).copy()
+    if size == 0:
+        for n, v in zip(lens, V):
+            v[:n + t - 1] = 0
+        sees[:, 0, t - 1] = False
+    case = qc.Case("e4m3", 64, 1, 64, K, V, lens, None, t, 1100)
+    q = qc.rows((3, t, group, 64), 19, qc.TYPES[kind][0]) * 0.1
+    out, lse = case.call(q, sees, 0.02)
+    if kind == "fp16" and size:                              # outputs beyond fp16: the log-sums alone
+        for b, n in enumerate(lens):
+            for i in range(t):
+                seen = [*range(n), n + i]
+                s = 0.02 * (qc.host(q)[b, i] @ case.K[b][seen, 0].T)
+                want = np.log(np.exp(s).sum(-1))
+                e = 0.02 * 72 * qc.U * (np.abs(qc.host(q)[b, i]) @ np.abs(case.K[b][seen, 0]).T).max() + 4 * qc.U * np.abs(s).max()
+                assert (np.abs(qc.host(lse)[b, i] - want) <= e + qc.U * np.abs(want) + (len(seen) / 4 + 64) * qc.U).all()
+    else:
+        case.check(q, out, lse, sees, 0.02, floor=floor(t, group))
