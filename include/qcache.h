@@ -144,8 +144,8 @@ int qc_read(qc_ctx *ctx, int type, int64_t n, const int64_t *slots, const void *
  * (n_nodes * n_q_heads / n_heads) and from 1,024 places (max_len + n_nodes) on, those that are light beside the row's
  * largest are held to 2^-29 of it instead, so that an element which is zero wherever p s is large may lose that much
  * a place. Below, rows whose values are small beside others of the sequence are summed in float32, and an element that
- * is zero in a row's heavy places may lose 2^-20 of the row's largest element for each light one. Weights below 2^-100 of
- * the row's heaviest, and values whose scale is below 2^-100 of the largest of their sequence, may count as zero.
+ * is zero in a row's heavy places may lose 2^-20 of the row's largest element for each light one. Products p s
+ * below 2^-90 of the row's heaviest weight times the largest scale of its sequence lose bits, down to none.
  * n_seq <= 65,535, and n_seq * n_nodes * n_q_heads < 2^31. Results do not depend on timing.
  */
 int qc_attend(qc_ctx *ctx, int type, int64_t n_seq, int n_nodes, int n_q_heads, const void *q, int64_t q_seq,

@@ -174,3 +174,33 @@ def test_log_sums_do_not_hang_on_the_values(kind, t, group, size):
                 assert (np.abs(qc.host(lse)[b, i] - want) <= e + qc.U * np.abs(want) + (len(seen) / 4 + 64) * qc.U).all()
     else:
         case.check(q, out, lse, sees, 0.02, floor=floor(t, group))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3", "e2m1"])
+@pytest.mark.parametrize("d,page,group", [(64, 16, 3), (128, 16, 1), (128, 64, 3), (64, 256, 8), (128, 256, 8)])
+@pytest.mark.parametrize("kind", ["fp16", "bf16"])
+def test_rows_taken_again(fmt, d, page, group, kind):
+    """Few rows, all but the first node's far below the unit: within one run of tiles and over several, under a tree, over
+    absent pages, several heads."""
+    import qcache_cases as qc
+    t, lens = 5, [3001, 20, 0, 27]
+    K = [qc.rows((n + t, 2, d), 20 + i) for i, n in enumerate(lens)]
+    V = [qc.rows((n + t, 2, d), 30 + i) * 2.0 ** -3 for i, n in enumerate(lens)]
+    for v, n in zip(V, lens):
+        v[n, 1] *= 2.0 ** 70
+    sees = np.broadcast_to(np.tril(np.ones((t, t), bool)), (4, t, t)).copy()
+    sees[:, 1:, 0] = False
+    sees[2, 3] = False
+    case = qc.Case(fmt, d, 2, page, K, V, lens, [5, 4, 5, 5], t, 3001)
+    q = qc.rows((4, t, 2 * group, d), 40, qc.TYPES[kind][0])
+    skip = {(b, 0) for b in range(4)} if kind == "fp16" else ()
+    out, lse = case.call(q, sees)
+    case.check(q, out, lse, sees, skip=skip, floor=2.0 ** -20)
+    table, gone = case.table.copy(), [3, 7]
+    table[0, gone] = [-1, len(case.pages)]
+    out, lse = case.call(q, sees, table=table)
+    import random_access_kv_gb300 as fq
+    assert fq.qc_status(case.ctx) == fq.QC_FLAG_RANGE
+    keep = ~np.isin(np.arange(3001 + t) // page, gone)
+    case.K[0], case.V[0], case.lens[0] = case.K[0][keep], case.V[0][keep], int(keep[:3001].sum())
+    case.check(q, out, lse, sees, skip=skip, floor=2.0 ** -20)
