@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(32 * (4 * NM + 5 + kProducers), 1) attend_tc(c
     using I = Item<FMT, D>;
     // A weight to 11 bits, and for fp16 outputs what that leaves, to 22: with 11 an fp16 output was 1.5 to 1.7 times
     // as far from 64 bits as its own rounding is, bf16's eight bits hide it. (Trees of 16, e4m3: 31.5 us with one
-    // term, 35.3 with two, 36 with units of the rows' own.)
+    // term, 35.3 with two, 36.6 with units of the rows' own.)
     constexpr int kTerms = std::is_same<T, __half>::value ? 2 : 1;
     constexpr int kOp = kOperand<D>, kSoft = 4 * NM, kConv = kSoft, kProducer = kSoft + 4, kMma = kProducer + kProducers;
     extern __shared__ __align__(1024) unsigned char smem[];
