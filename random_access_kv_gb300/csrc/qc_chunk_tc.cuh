@@ -701,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
                     tmem_st32(o_col + 32 * i, o);
                 }
+                tmem_wait_st();                 // a tile may rescale twice, and loads are not ordered behind stores by themselves
             };
             for (int i = 0; ok && i < (active ? tiles : 0); ++i) {
                 const int tile = alone ? run.place(run.tile + 2 * i + rt) : from - i, c = (it + run.place(tile) - run.tile) & 3;
