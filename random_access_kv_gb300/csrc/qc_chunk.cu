@@ -28,9 +28,12 @@ __global__ void __launch_bounds__(kThreads) chunk_join(const Chunk p, const Chun
     PartLine line = parts.lines[first];
     if (!line.what) line = parts.lines[--first];
     if (!(line.what & kOpens) || (line.what & kCloses)) return;
+    // a line leads to rows of the call's own tensors or nowhere, whatever the workspace holds
+    if (line.b < 0 || line.b >= p.n_seq || line.kv < 0 || line.kv >= p.g.heads) return;
+    const Sequence s = sequence(p, line.b, false);
+    if (line.run < 0 || line.run >= runs_of(p, s, parts.rows)) return;
     int last = unit + 1;
     while (last < units - 1 && !(parts.lines[2 * (int64_t)last].what & kCloses)) ++last;
-    const Sequence s = sequence(p, line.b, false);
     const int rows = min(s.news * p.group - line.run * parts.rows, parts.rows);
     for (int r = (int)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += (int)gridDim.y * (kThreads / 32)) {
         float m = -INFINITY, l = 0.f, o[N] = {};

@@ -55,10 +55,7 @@ __device__ __forceinline__ int2 tiles_of_rows(const Chunk &p, const Sequence &s,
     return make_int2(sees(p, s, s.len + i0).x / kChunkTile, (sees(p, s, s.len + i1).y + kChunkTile - 1) / kChunkTile);
 }
 
-template <int ROWS>
-__device__ __forceinline__ int runs_of(const Chunk &p, const Sequence &s) {
-    return (s.news * p.group + ROWS - 1) / ROWS;
-}
+__device__ __forceinline__ int runs_of(const Chunk &p, const Sequence &s, int rows) { return (s.news * p.group + rows - 1) / rows; }
 
 // A unit's place in the order of tiles.
 struct ChunkWalk {
@@ -84,7 +81,7 @@ struct ChunkWalk {
     __device__ __forceinline__ void next(const Chunk &p) {
         left -= end() - tile;
         if (left <= 0) return;
-        if (++run >= runs_of<ROWS>(p, s)) {
+        if (++run >= runs_of(p, s, ROWS)) {
             run = 0;
             if (++kv >= p.g.heads) {
                 kv = 0;
@@ -126,7 +123,7 @@ __device__ __forceinline__ Sequence of_lane(const Sequence &s, int l) {
 // Tiles of one head of this lane's sequence (one warp). Few runs are counted by the lane, many by the warp.
 template <int ROWS>
 __device__ __forceinline__ int64_t head_tiles(const Chunk &p, const Sequence &s, int lane) {
-    const int runs = runs_of<ROWS>(p, s);
+    const int runs = runs_of(p, s, ROWS);
     int64_t sum = 0;
     if (runs <= 4)
         for (int i = 0; i < runs; ++i) {
@@ -136,7 +133,7 @@ __device__ __forceinline__ int64_t head_tiles(const Chunk &p, const Sequence &s,
     for (uint32_t many = __ballot_sync(0xffffffffu, runs > 4); many; many &= many - 1) {
         const int l = __ffs(many) - 1;
         const Sequence o = of_lane(s, l);
-        const int n = runs_of<ROWS>(p, o);
+        const int n = runs_of(p, o, ROWS);
         int64_t mine = 0;
         for (int i = lane; i < n; i += 32) {
             const int2 t = tiles_of_rows(p, o, i * ROWS, ROWS);
@@ -178,7 +175,7 @@ __device__ __forceinline__ ChunkWalk find_run(const Chunk &p, int unit, int unit
         w.s = of_lane(s, l);
         w.kv = (int)(at / head);
         at -= w.kv * head;
-        const int runs = runs_of<ROWS>(p, w.s);
+        const int runs = runs_of(p, w.s, ROWS);
         for (int i0 = 0; i0 < runs; i0 += 32) {
             const int2 t = tiles_of_rows(p, w.s, (i0 + lane) * ROWS, ROWS);
             const int64_t n = i0 + lane < runs ? t.y - t.x : 0, to = warp_upto(n, lane);
@@ -200,7 +197,8 @@ __device__ __forceinline__ ChunkWalk find_run(const Chunk &p, int unit, int unit
 }
 
 // The workspace: for each of 2 units' parts a line, then values [rows][d], then (reference, sum) [rows]. A unit's first
-// job is part 2 unit, the last one of its run, if that is another, part 2 unit + 1.
+// job is part 2 unit, the last one of its run, if that is another, part 2 unit + 1. A unit's lines are emptied before
+// anything of it can give up, and written when all of its copies are under way: so a line is this call's, or empty.
 struct PartLine {
     int b, kv, run;
     int what;               // 0: no part; else kHolds, with kOpens where it has the job's first tile, kCloses its last

@@ -415,6 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducer) {
         const ChunkWalk w = find_run<ROWS>(p, unit, plan.units, blockIdx.x == 0, lane);
         if (lane == 0) sm.start = w;
+        if (lane < 2 && cta == 0) parts.lines[2 * unit + lane] = {};        // of an earlier call, or of none
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
