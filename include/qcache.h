@@ -236,8 +236,8 @@ int64_t qc_attend_workspace(const qc_ctx *ctx, int64_t n_seq, int n_nodes, int n
  * holds a NaN or an infinity, or (without a cap) a score above float32's range, has out = NaN and lse = NaN. So may one that
  * sees a key row whose scale times `scale` (over cap, where there is one) is 2^124 or more.
  * Products take the codes and q as they are, exactly; sums are float32. Weights times their value rows' scales are rounded to
- * 11 bits for QC_BF16 and to 22 for QC_F16, or by 2^-29 of the row's largest one where that is more. Value rows' scales above
- * 2^106 count as 2^106. lse comes from the weights before that rounding.
+ * 11 bits for QC_BF16 and to 22 for QC_F16, or by 2^-29 of the row's largest one where that is more. lse comes from the
+ * weights before that rounding. Value rows may have any scale that qc_write makes (jobs that see one above 2^44 take longer).
  * n_seq <= 65,535, n_tokens * n_q_heads <= 2^31 - 512, max_len + max_new <= 2^31 - 4,096. Results do not depend on timing.
  */
 int qc_attend_chunk(qc_ctx *ctx, int type, int64_t n_seq, int64_t n_tokens, int n_q_heads, const void *q, int64_t q_token,

@@ -2,9 +2,9 @@
 // leaves.
 //
 // The division follows lengths that only the device knows: all tiles of all (run of rows, head) jobs, as the rows' windows and the
-// prefixes leave them, are dealt to the pairs of CTAs in equal runs. A pair's open jobs at either end go to the workspace as
-// float32 sums; the joining launch starts while the first still runs, and adds them in the order of the units, so that results
-// do not depend on timing. A unit's rows are shared out over several blocks too, two to
+// prefixes leave them, are dealt to the pairs of CTAs in equal runs. A pair's open jobs at either end go to the workspace: the
+// float32 outputs of their own places, and the sums of weights beside them. The joining launch starts while the first still runs, and
+// adds them, each by its share of the weights, in the order of the units, so that results do not depend on timing. A unit's rows are shared out over several blocks too, two to
 // a warp, since few units may hold all open jobs.
 #include <math.h>
 
@@ -36,26 +36,43 @@ __global__ void __launch_bounds__(kThreads) chunk_join(const Chunk p, const Chun
     while (last < units - 1 && !(parts.lines[2 * (int64_t)last].what & kCloses)) ++last;
     const int rows = min(s.news * p.group - line.run * parts.rows, parts.rows);
     for (int r = (int)blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); r < rows; r += (int)gridDim.y * (kThreads / 32)) {
-        float m = -INFINITY, l = 0.f, o[N] = {};
-        for (int c = unit + lane; c <= last; c += 32) m = fmaxf(m, parts.stat(c == unit ? first : 2 * (int64_t)c, r)->x);
+        auto part_of = [&](int c) { return c == unit ? first : 2 * (int64_t)c; };
+        auto stat = [&](int c) { return c <= last ? *parts.stat(part_of(c), r) : make_float2(-INFINITY, 0.f); };
+        // lane i has the sums of the i-th part, and of every 32nd from there
+        const float2 mine = stat(unit + lane);
+        float m = mine.x, l = 0.f, o[N] = {};
+        for (int c = unit + 32 + lane; c <= last; c += 32) m = fmaxf(m, stat(c).x);
 #pragma unroll
         for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
         const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-        for (int c = unit; c <= last; ++c) {
-            const int64_t part = c == unit ? first : 2 * (int64_t)c;
-            const float2 st = *parts.stat(part, r);
-            const float w = exp2f(st.x - ref);
-            const float *v = parts.row(part, r) + lane * N;
-            l = fmaf(st.y, w, l);
+        // a part's sum of weights in the largest reference's unit, as two factors: either may be far from 1
+        auto weight = [&](float2 st) {
+            const float t = st.x - ref, a = fmaxf(t, -100.f);
+            return make_float2(exp2f(a), exp2f(t - a) * st.y);
+        };
+        float2 w = weight(mine);
+        l = w.x * w.y;
+        for (int c = unit + 32 + lane; c <= last; c += 32) {
+            const float2 x = weight(stat(c));
+            l = fmaf(x.x, x.y, l);
+        }
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = fmaf(v[i], w, o[i]);
+        for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const float by = l != 0.f ? 1.f / l : 0.f;                  // a NaN goes out
+        for (int c0 = unit; c0 <= last; c0 += 32) {
+            if (c0 > unit) w = weight(stat(c0 + lane));
+            const float share = w.y * by;
+            const int n = min(last - c0 + 1, 32);
+#pragma unroll 4
+            for (int i = 0; i < n; ++i) {
+                const float *v = parts.row(part_of(c0 + i), r) + lane * N;
+                const float a = __shfl_sync(0xffffffffu, w.x, i), b = __shfl_sync(0xffffffffu, share, i);
+#pragma unroll
+                for (int k = 0; k < N; ++k) o[k] = fmaf(v[k] * a, b, o[k]);
+            }
         }
         const int at = line.run * parts.rows + r, token = at / p.group;
         const int64_t out_row = (int64_t)(s.first + token) * p.n_q_heads + line.kv * p.group + (at - token * p.group);
-        const float by = l != 0.f ? 9.5367431640625e-7f / l : 0.f;      // 2^-20: the values' scales' unit; a NaN goes out
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] *= by;
         store_row<T, N>(static_cast<T *>(p.out) + out_row * D + lane * N, o);
         if (p.lse && lane == 0) p.lse[out_row] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }

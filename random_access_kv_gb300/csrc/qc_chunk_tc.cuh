@@ -23,6 +23,15 @@
 // with one, an output was 1.5 to 1.7 times as far from 64 bits as its own rounding is. Value rows of zeros (s_v = 0) have no
 // P; their weights are summed apart, with a reference of their own.
 //
+// Range. In a sum of weights p is P / s_v, and float32 has room for that as long as s_v is neither too small nor too large.
+// qc_write makes scales of 2^-112 to 2^121. In units of 2^-20, as here, the small ones give p of 2^107 at most; above 2^64
+// weights as heavy as the heaviest would come too near to 2^-126. So from the first tile with such a scale on, a warp sums all
+// of a job's weights apart, by the scores' own largest, and takes its tiles step by step; P is then made with 2^64 at
+// the weight and 2^-64 at the scale. (Caches in earnest hold no values of 2^51.) Where sums of unlike references meet, as a
+// reference moves, in a row's two warps, in units' parts, factors below 2^-100 are taken in two steps, so that none is lost.
+// That costs the calls that have none of it up to 5 % (single tokens over windows 335 -> 343 us, short prompts 108 -> 113), for
+// the code that they step over; long chunks gain one.
+//
 // As M moves seldom, weights are made from scores at once, without a look for the largest first, and looked over afterwards;
 // where one passes the limit, or some place is not seen, that half is done again, step by step.
 //
@@ -56,8 +65,9 @@ static_assert(kTile == kChunkTile, "tiles of places");
 constexpr float kSoon = 512.f;
 constexpr float kMostLog = 15.9f, kMostP = 61147.f;     // the largest product that is let to fp16, and its log2
 constexpr float kTop = 4.f;              // a new reference puts the largest one at 2^kTop, or up to twice that
-constexpr float kScaleUnit = 1048576.f, kMostScale = 8.507059173023462e37f;       // values' scales are held times 2^20, up to 2^126
-constexpr float kZeroRoom = 60.f;       // weights of rows of zeros are up to 2^kZeroRoom in units of the others'
+constexpr float kScaleUnit = 1048576.f;  // values' scales are held times 2^20
+// Those above 2^44, 2^kHugeLog in that unit, are huge, and held times 2^-44 (up to 2^84: qc_write makes none above that).
+constexpr float kHuge = 17592186044416.f, kHugeUnit = 5.684341886080802e-14f, kHugeLog = 64.f, kMostHuge = 1.9342813113834067e25f;
 constexpr int kMostStages = 4;
 constexpr int kConverters = 4, kProducerWarps = 2;
 
@@ -115,7 +125,8 @@ struct Small {
     // argument), and the values' scales; and log2 of those
     alignas(16) float kv[4][kTile / 2][4];
     alignas(16) float lv[4][kTile];
-    alignas(16) uint32_t exist[4][4], zero[4][4];       // places that exist: with values, and with rows of zeros for them
+    // places that exist: with values of no huge scale, with values of any, and with rows of zeros for them
+    alignas(16) uint32_t exist[4][4], product[4][4], zero[4][4];
     alignas(16) float4 other[128];      // of a row that two warps share: the second's references and sums
     ChunkWalk start;
     uint32_t tmem;
@@ -182,6 +193,27 @@ __device__ __forceinline__ uint64_t sdesc_sw64_mn(uint32_t saddr) {
 
 // floor(log2(x)), x > 0 and normal
 __device__ __forceinline__ float log2_below(float x) { return (float)((int)(__float_as_uint(x) >> 23) - 127); }
+// 2^t as two factors, for t from -226 to 226
+__device__ __forceinline__ float2 power_of_2(float t) {
+    const float a = fminf(fmaxf(t, -100.f), 100.f);
+    return make_float2(ex2(a), ex2(t - a));
+}
+// A sum of weights, w 2^ref. One that is a NaN stays one.
+struct Sum {
+    float ref, w;
+};
+// a + b with each at its own height first, so that neither is lost where references are far from the sums
+__device__ __forceinline__ Sum joined(Sum a, Sum b) {
+    if (b.w == 0.f) return a;
+    if (a.w == 0.f) return b;
+    auto level = [](Sum x) {
+        if (!(x.w < INFINITY)) return x;
+        return Sum{x.ref + log2_below(x.w), __uint_as_float((__float_as_uint(x.w) & 0x007fffffu) | 0x3f800000u)};
+    };
+    a = level(a), b = level(b);
+    const float ref = fmaxf(a.ref, b.ref);
+    return {ref, a.w * ex2(a.ref - ref) + b.w * ex2(b.ref - ref)};
+}
 __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
@@ -459,14 +491,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         auto is_there = [&](int i) { return tile * kTile + i < places && !((bad >> (i >> 4)) & 1u); };
                         const bool good = is_there(t);
                         const float *scale = reinterpret_cast<const float *>(st + R::kScales);
-                        const float vs = good ? fminf(scale[kTile + t] * kScaleUnit, kMostScale) : 0.f;
+                        const float sv = good ? scale[kTile + t] : 0.f;
+                        const bool some = sv > 0.f, huge = sv > kHuge;
+                        const float vs = !some ? 0.f : huge ? fminf(sv * kHugeUnit, kMostHuge) : sv * kScaleUnit;
                         sm.kv[it & 3][t >> 1][t & 1] = good ? scale[t] * up : 0.f;
                         sm.kv[it & 3][t >> 1][2 + (t & 1)] = vs;
-                        sm.lv[it & 3][t] = vs > 0.f ? log2f(vs) : 0.f;
-                        const uint32_t e = __ballot_sync(0xffffffffu, good && vs > 0.f), z = __ballot_sync(0xffffffffu, good && !(vs > 0.f));
+                        sm.lv[it & 3][t] = some ? log2f(vs) + (huge ? kHugeLog : 0.f) : 0.f;
+                        const uint32_t e = __ballot_sync(0xffffffffu, some && !huge), z = __ballot_sync(0xffffffffu, good && !some),
+                                       v = __ballot_sync(0xffffffffu, some);
                         if (lane == 0) {
                             sm.exist[it & 3][quarter] = e;
                             sm.zero[it & 3][quarter] = z;
+                            sm.product[it & 3][quarter] = v;
                         }
                         // a place and half of its row
                         const int i = t & 63, h = t >> 6;
@@ -642,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;                     // 32 lanes of TMEM per warp
         const uint32_t s_col = tmem + lanes + rt * kTile, o_col = tmem + lanes + 256 + rt * D;
         int n = 0;                              // tiles that the row tile has had
-        for (int segment = 0, joined = 0; run.left > 0; run.template next<ROWS>(p), ++segment) {
+        for (int segment = 0, joins = 0; run.left > 0; run.template next<ROWS>(p), ++segment) {
             const Sequence &s = run.s;
             const bool alone = solo(p, run);
             const int part_row = (alone ? 0 : rt * 256) + cta * 128 + (threadIdx.x & 127);         // of the job's rows
@@ -652,8 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t out_row = (int64_t)(s.first + token) * p.n_q_heads + run.kv * p.group + h;
             const int t = s.len + token;
             const int2 seen = sees(p, s, t);
-            // places that all of the warp's rows see
-            const int lo = __reduce_max_sync(0xffffffffu, there ? seen.x : 0), hi = __reduce_min_sync(0xffffffffu, there ? seen.y : INT32_MAX);
+            // places that all of the warp's rows see; lo is kApart once the warp sums all weights apart: then no tile is among them
+            constexpr int kApart = INT32_MAX;
+            int lo = __reduce_max_sync(0xffffffffu, there ? seen.x : 0);
+            const int hi = __reduce_min_sync(0xffffffffu, there ? seen.y : INT32_MAX);
             const int2 of = tiles_of_rows(p, s, run.run * ROWS + rt * 256, 256);
             if (active && !(alone && rt)) {
                 const T *q = static_cast<const T *>(p.q) + (s.first + token) * p.q_token + (run.kv * p.group + h) * p.q_head;
@@ -679,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float top_score = X & kCap ? p.cap * kLog2e : 1.f;
             float m = -INFINITY;
             float2 l = make_float2(0.f, 0.f);
-            float mz = -INFINITY, lz = 0.f;     // of rows of zeros
+            float mz = -INFINITY, lz = 0.f;     // of weights that are summed apart
             float last = 0.f;                   // the row's largest product of the last tile
             // the last of its tiles first: what a bias by distance favours, so that references seldom move
             const int from = min(run.place(run.tile), of.y - 1), to = max(run.place(end - 1), of.x);
@@ -691,9 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     arrive_first(&bar.p_ready[rt][1]);
                 }
             }
-            // the sums so far, in another unit
+            // the products' sums so far, in another unit
             auto rescale = [&](float by) {
-                l = mul2f(l, make_float2(by, by));
 #pragma unroll 1
                 for (int i = 0; i < D / 32; ++i) {
                     uint32_t o[32];
@@ -715,7 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // tile's scores were made
                     const float up = last > kSoon ? log2_below(last) - kTop : 0.f;
                     m += up;
-                    rescale(ex2(-up));
+                    const float by = ex2(-up);
+                    l = mul2f(l, make_float2(by, by));
+                    rescale(by);
                 }
                 last = 0.f;
                 const uint4 ex4 = *reinterpret_cast<const uint4 *>(sm.exist[c]);
@@ -812,8 +851,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (again) {
                             // step by step: the largest product, the reference, the weights; 32 places at a time
-                            const uint2 ex = *reinterpret_cast<const uint2 *>(&sm.exist[c][2 * half]);
-                            const uint2 ze = *reinterpret_cast<const uint2 *>(&sm.zero[c][2 * half]);
+                            const uint2 ex = *reinterpret_cast<const uint2 *>(&sm.product[c][2 * half]);
+                            const uint2 no = *reinterpret_cast<const uint2 *>(&sm.exist[c][2 * half]);
+                            uint2 ze = *reinterpret_cast<const uint2 *>(&sm.zero[c][2 * half]);
+                            const bool any_huge = ex.x != no.x || ex.y != no.y;
+                            if (any_huge || lo == kApart) {
+                                // all weights are summed apart, and those that were not go there; what l has from here on says nothing
+                                if (lo != kApart) {
+                                    const Sum z = joined({m, l.x + l.y}, {mz, lz});
+                                    mz = z.ref, lz = z.w;
+                                    lo = kApart;
+                                }
+                                l = make_float2(0.f, 0.f);
+                                ze.x |= ex.x, ze.y |= ex.y;
+                            }
                             const float2 *lv = reinterpret_cast<const float2 *>(&sm.lv[c][64 * half]);
                             // which of places 32 j .. the row sees
                             auto sees_of = [&](int j) {
@@ -851,7 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const bool move = top > m + kMostLog;
                             if (__any_sync(0xffffffffu, move)) {
                                 const float m2 = move ? top - kTop : m;
-                                const float by = m == m2 ? 1.f : ex2(m - m2);
+                                const float d = m == m2 ? 0.f : m - m2, by = ex2(d);
+                                const float2 f = power_of_2(d);
+                                l = mul2f(mul2f(l, make_float2(f.x, f.x)), make_float2(f.y, f.y));
                                 m = m2;
                                 // the first half's products may still be added to the sums
                                 if (half) ok = warp_poll(&bar.o_done[rt], n + i);
@@ -863,22 +916,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float neg = m == -INFINITY ? 0.f : -m;
                             uint32_t most = 0;
                             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                            auto weigh_half = [&](auto with_huge) {
 #pragma unroll 1
-                            for (int j = 0; j < 2; ++j) {
-                                uint32_t x32[32], w[16 * kTerms];
-                                tmem_ld32_nowait(s_col + 64 * half + 32 * j, x32);
-                                const uint32_t see = sees_of(j) & (j ? ex.y : ex.x);
-                                tmem_wait_ld();
+                                for (int j = 0; j < 2; ++j) {
+                                    uint32_t x32[32], w[16 * kTerms];
+                                    tmem_ld32_nowait(s_col + 64 * half + 32 * j, x32);
+                                    const uint32_t see = sees_of(j) & (j ? ex.y : ex.x), big = j ? ex.y ^ no.y : ex.x ^ no.x;
+                                    tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    float2 x = score(pair_of(x32, i), 16 * j + i, make_float2(neg, neg));
-                                    if (!((see >> (2 * i)) & 1u)) x.x = -INFINITY;
-                                    if (!((see >> (2 * i)) & 2u)) x.y = -INFINITY;
-                                    weigh(x, 16 * j + i, sum[i & 1], w + i);
-                                    most = max2(most, w[i]);
+                                    for (int i = 0; i < 16; ++i) {
+                                        float2 x = score(pair_of(x32, i), 16 * j + i, make_float2(neg, neg));
+                                        if (!((see >> (2 * i)) & 1u)) x.x = -INFINITY;
+                                        if (!((see >> (2 * i)) & 2u)) x.y = -INFINITY;
+                                        if constexpr (decltype(with_huge)::value) {
+                                            if ((big >> (2 * i)) & 1u) x.x += kHugeLog;
+                                            if ((big >> (2 * i)) & 2u) x.y += kHugeLog;
+                                        }
+                                        weigh(x, 16 * j + i, sum[i & 1], w + i);
+                                        most = max2(most, w[i]);
+                                    }
+                                    put(s_col + 64 * half + 32 * j, w);
                                 }
-                                put(s_col + 64 * half + 32 * j, w);
-                            }
+                            };
+                            if (any_huge)
+                                weigh_half(std::true_type{});
+                            else
+                                weigh_half(std::false_type{});
                             l = add2f(l, add2f(sum[0], sum[1]));
                             const float2 top2 = float2_of(most);
                             last = fmaxf(last, fmaxf(top2.x, top2.y));
@@ -895,39 +958,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             float4 *other = &sm.other[threadIdx.x & 127];
             if (alone && rt) {                  // the other warp with these rows joins both
-                *other = make_float4(m, l.x + l.y, mz, lz);
+                *other = make_float4(m, lo == kApart ? 0.f : l.x + l.y, mz, lz);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.join);
             } else if (active) {
                 const bool whole = run.tile == run.first && end == run.last;
                 const int64_t part = 2 * (int64_t)unit + (segment ? 1 : 0);
-                float total = l.x + l.y, up = 1.f, up1 = 0.f;       // of this warp's sums, and of the other's
-                bool product = m > -INFINITY, product1 = false;
+                // of this warp's products, and of the other's: are there any, and their factors in the larger reference's unit
+                const bool product = m > -INFINITY;
+                bool product1 = false;
+                float up = 1.f, up1 = 0.f, most = m;
+                Sum sum = {m, lo == kApart ? 0.f : l.x + l.y}, apart = {mz, lz};
+                float2 unit2 = make_float2(1.f / kScaleUnit, 1.f);      // of the products, in that of the weights
                 if (alone) {
-                    ok = warp_poll(&bar.join, joined);
+                    ok = warp_poll(&bar.join, joins);
                     if (!ok) break;
                     const float4 x = *other;
                     product1 = x.x > -INFINITY;
-                    const float most = fmaxf(m, x.x), most_z = fmaxf(mz, x.z);
-                    up = product ? ex2(m - most) : 0.f;
-                    up1 = product1 ? ex2(x.x - most) : 0.f;
+                    most = fmaxf(m, x.x);
+                    const float2 f = product ? power_of_2(m - most) : make_float2(0.f, 0.f);
+                    const float2 f1 = product1 ? power_of_2(x.x - most) : make_float2(0.f, 0.f);
+                    up = f.x * f.y, up1 = f1.x * f1.y;
                     // (a NaN has no reference, and goes out)
-                    total = (product ? total * up : isnan(total) ? total : 0.f) + (product1 ? x.y * up1 : isnan(x.y) ? x.y : 0.f);
-                    lz = (mz > -INFINITY ? lz * ex2(mz - most_z) : lz) + (x.z > -INFINITY ? x.w * ex2(x.z - most_z) : x.w);
-                    m = most;
-                    mz = most_z;
+                    const Sum both = {most, (product ? sum.w * f.x * f.y : isnan(sum.w) ? sum.w : 0.f) +
+                                                (product1 ? x.y * f1.x * f1.y : isnan(x.y) ? x.y : 0.f)};
+                    if (__any_sync(0xffffffffu, lz != 0.f || x.w != 0.f)) {
+                        apart = joined(apart, {x.z, x.w});
+                        if (apart.w != 0.f) sum = joined(sum, {x.x, x.y});
+                    }
+                    if (apart.w == 0.f) sum = both;
                 }
-                const bool some_product = product || product1;
-                float down = 1.f;
-                if (lz != 0.f) {
-                    // the weights of rows of zeros, in the others' unit, or both in one that holds them
-                    const float d = some_product ? mz - m : kZeroRoom, x = fmaxf(d - kZeroRoom, 0.f);
-                    down = ex2(-0.5f * x);
-                    total = total * down * down + lz * ex2(d - x);
-                    m = some_product ? m + x : mz - kZeroRoom;
+                if (__any_sync(0xffffffffu, apart.w != 0.f)) {
+                    sum = joined(sum, apart);
+                    const float2 f = power_of_2(most == sum.ref ? 0.f : most - sum.ref);
+                    unit2 = make_float2(f.x * (1.f / kScaleUnit), f.y);
                 }
-                const bool some = total != 0.f, odd = isnan(total);         // a NaN goes out
-                const float by = whole ? (some ? 1.f / total * (1.f / kScaleUnit) : 0.f) : 1.f;
+                const float total = sum.w;
+                const bool some = total != 0.f, odd = isnan(total);
+                const float by = some ? 1.f / total : 0.f;
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
                     uint32_t o[16], o1[16];
@@ -940,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 16; ++i) {
                             float x = product ? __uint_as_float(o[i]) * up : 0.f;
                             if (product1) x = fmaf(__uint_as_float(o1[i]), up1, x);
-                            v[i] = odd ? total : some ? x * down * down * by : 0.f;
+                            v[i] = odd ? total : some ? x * by * unit2.x * unit2.y : 0.f;
                         }
                         if (whole) {
                             store_row<T, 16>(static_cast<T *>(p.out) + out_row * D + 16 * c, v);
@@ -953,12 +1021,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (there) {
                     if (!whole)
-                        *parts.stat(part, part_row) = make_float2(some ? m : -INFINITY, total);
+                        *parts.stat(part, part_row) = make_float2(some ? sum.ref : -INFINITY, total);
                     else if (p.lse)
-                        p.lse[out_row] = some ? (m + log2f(total)) * kLn2 : -INFINITY;
+                        p.lse[out_row] = some ? (sum.ref + log2f(total)) * kLn2 : -INFINITY;
                 }
             }
-            joined += alone;
+            joins += alone;
             tc_fence_before();
             it += end - run.tile;
         }
