@@ -130,8 +130,8 @@ int qc_norm_rope_axes(qc_ctx *ctx, int type, int64_t n, const void *q, int hq, i
  *   held, held_out : device int32 [n_seq], or both NULL: the pages that each request holds, its table's first held[b]
  *                entries, before the call and after it (in another place); fewer than its tokens fill count as those, more
  *                than width as width, with QC_FLAG_RANGE for negative ones and these.
- * Where the free pages do not suffice, the pages that are wanting are -1 in the table, their tokens' slots are -1,
- * taken_out is n_free, and QC_FLAG_PAGES is set.
+ * Where the free pages do not suffice, the pages that are wanting are -1 in the table and not in held_out, their tokens'
+ * slots are -1, taken_out is n_free, and QC_FLAG_PAGES is set. The same step tried again with held = held_out asks for them.
  * n_seq <= 65,535, n_tokens < 2^31, width <= 2^26. Results do not depend on timing.
  */
 int qc_plan(qc_ctx *ctx, int64_t n_seq, const int32_t *lens, const int32_t *news, const int32_t *free_pages, int64_t n_free,

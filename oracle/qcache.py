@@ -157,7 +157,7 @@ def plan(lens, news, free_pages, taken, table, n_tokens, page, held=None):
             odd |= not 0 <= held[b] <= width
             have = held[b] = min(max(held[b], min(have, width)), width)
         for k in range(have, min(-(-(n + t) // page), width)):
-            if held is not None:
+            if held is not None and taken < n_free:           # a page that is wanting is not held
                 held[b] = k + 1
             lack |= taken >= n_free
             table[b, k] = free_pages[taken] if taken < n_free else -1

@@ -115,12 +115,15 @@ __global__ void __launch_bounds__(kThreads) plan(const Plan p) {
     };
 
     if (first) {
-        int64_t at = base_rows;
+        int64_t at = base_rows, page = base_pages;
         for (int b = b0; b < b1; ++b) {
             p.starts[b] = (int32_t)(at < p.n_tokens ? at : p.n_tokens);
             const Request r = request(p, b, false);
             at += r.news;
-            if (p.held) p.held_out[b] = (int32_t)(r.have + r.need);
+            // of the pages that it wants it holds those that there are: a later try asks for the others again
+            const int64_t there = left - page;
+            if (p.held) p.held_out[b] = (int32_t)(r.have + (there >= r.need ? r.need : there > 0 ? there : 0));
+            page += r.need;
         }
         if (tid == 0) {
             p.starts[p.n_seq] = (int32_t)(all_rows < p.n_tokens ? all_rows : p.n_tokens);
