@@ -400,21 +400,17 @@ def qc_page_bytes(ctx: CacheContext) -> int:
     return int(b)
 
 
-def qc_norm_rope(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, rot: int, interleaved: bool, q_out, k_out,
-                 stream=None) -> None:
-    """q [n, hq, d] and k [n, hk, d] (either may be None), strided; w_q, w_k float32 [d] or None; pos int64
-    [n]; table float32 [max_pos, rot]; q_out, k_out like q and k (themselves, too)."""
-    _norm_rope(ctx, q, k, w_q, w_k, eps, pos, table, rot, None, interleaved, q_out, k_out, stream)
-
-
 def qc_norm_rope_axes(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, sections, interleaved: bool, q_out, k_out,
                       stream=None) -> None:
     """As qc_norm_rope; sections: how many pairs each axis turns; pos int64 [axes, n]; table float32 [max_pos, 2 sum(sections)]."""
-    _norm_rope(ctx, q, k, w_q, w_k, eps, pos, table, 2 * sum(sections), (_int * len(sections))(*sections), interleaved, q_out, k_out, stream)
+    qc_norm_rope(ctx, q, k, w_q, w_k, eps, pos, table, 2 * sum(sections), interleaved, q_out, k_out, stream, (_int * len(sections))(*sections))
 
 
-def _norm_rope(ctx, q, k, w_q, w_k, eps, pos, table, rot, sections, interleaved, q_out, k_out, stream) -> None:
-    dev, d = ctx.device, ctx.d
+def qc_norm_rope(ctx: CacheContext, q, k, w_q, w_k, eps: float, pos, table, rot: int, interleaved: bool, q_out, k_out,
+                 stream=None, _sections=None) -> None:
+    """q [n, hq, d] and k [n, hk, d] (either may be None), strided; w_q, w_k float32 [d] or None; pos int64
+    [n]; table float32 [max_pos, rot]; q_out, k_out like q and k (themselves, too)."""
+    dev, d, sections = ctx.device, ctx.d, _sections
     ok, n, dtype = True, None, None
     if q is not None:
         qs, q0, o0 = q.shape, q.stride(), q_out.stride()
@@ -433,9 +429,9 @@ def _norm_rope(ctx, q, k, w_q, w_k, eps, pos, table, rot, sections, interleaved,
         raise ValueError("neither q nor k")
     if ok and rot:
         most = table.shape[0]
-        at = (n,) if sections is None else (len(sections), n)
-        ok = (pos.dtype is _I64 and pos.shape == at and pos.get_device() == dev and pos.is_contiguous() and table.dtype is _F32
-              and table.shape == (most, rot) and table.get_device() == dev and table.is_contiguous())
+        ok = (pos.dtype is _I64 and pos.shape == ((n,) if sections is None else (len(sections), n)) and pos.get_device() == dev
+              and pos.is_contiguous() and table.dtype is _F32 and table.shape == (most, rot) and table.get_device() == dev
+              and table.is_contiguous())
     kind = _QC_TYPES.get(dtype)
     if not ok or kind is None:
         rows = {}
