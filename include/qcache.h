@@ -232,6 +232,8 @@ int64_t qc_attend_workspace(const qc_ctx *ctx, int64_t n_seq, int n_nodes, int n
  *   cap       : 0 for none, or 2^-20 .. 2^40. window: 0 for none, or 1 .. 2^31 - 1.
  *   out       : device [n_tokens][n_q_heads][d], 16-byte aligned; lse: device float32 [n_tokens][n_q_heads], or NULL.
  *   workspace : as for qc_attend, at least qc_attend_chunk_workspace() bytes.
+ * Calls with max_new = 1 and no window, prefix, slopes or cap are qc_attend's with n_nodes = 1, which is made for few rows and
+ * takes less time; a tree of drafted tokens is qc_attend's too (here a token sees all new ones before it).
  * A row all of whose places lie in absent pages has out = 0 and lse = -inf. A row that sees a place and whose query
  * holds a NaN or an infinity, or (without a cap) a score above float32's range, has out = NaN and lse = NaN. So may one that
  * sees a key row whose scale times `scale` (over cap, where there is one) is 2^124 or more.
@@ -260,12 +262,14 @@ int64_t qc_attend_chunk_workspace(const qc_ctx *ctx, int64_t n_seq, int64_t n_to
  *   c is accepted if u[b][c] * q_r(x) * T < w(x), and the walk goes on from c;
  *   else w = max(w - T q_r, 0), T = sum of w, and the next child is asked. If T is 0, w is p_r again and the walk ends.
  * Where no child is left, the token that follows is the first k with w(0) + .. + w(k) > u[b][n_nodes] * (sum of w).
- * Accepted tokens and the last one are then distributed as the target's. Products and sums are as good as 64 bits'.
+ * Accepted tokens and the last one are then distributed as the target's. Products and sums are as good as 64 bits'. (The cached
+ * rows of an accepted path through a tree lie at its nodes' places; qc_read and qc_write move them to neighbouring ones.)
  *   type     : QC_F16, QC_BF16 or QC_F32, of p and q.
  *   n_nodes  : 1 .. 1024, that of the longest. vocab: 1 .. 2^24.
  *   p, q     : device, p [n_seq][n_nodes + 1][vocab], q [n_seq][n_nodes][vocab], the last index contiguous, the others'
  *              strides in elements. Negative or non-finite probabilities count as 0; one that is read sets
- *              QC_FLAG_NONFINITE. They need not sum to 1, nor start on 16-byte boundaries (faster if they do).
+ *              QC_FLAG_NONFINITE. They need not sum to 1, nor start on 16-byte boundaries (faster if they do). A w whose
+ *              sum is 2^127 or more may count as zero everywhere.
  *   tokens   : device int32 [n_seq][n_nodes]; a node whose token is outside [0, vocab) is not accepted, rejects
  *              nothing, and sets QC_FLAG_RANGE.
  *   parents  : device int32 [n_seq][n_nodes], -1 .. c - 1, or NULL for a chain (c - 1). Nodes with others are never

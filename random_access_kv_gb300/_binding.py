@@ -579,7 +579,7 @@ def qc_attend_chunk(ctx: CacheContext, pages, q, starts, table, lens, prefix, sl
     """q [n_tokens, n_q_heads, d], strided: the new tokens of all sequences, one sequence after another; starts int32
     [n_seq + 1]; table int32 [n_seq, >= (max_len + max_new) / page_tokens]; lens int32 [n_seq]; prefix int32 [n_seq] or
     None; slopes float32 [n_q_heads] or None; cap, window: 0 for none; out like q, contiguous; lse float32 [n_tokens,
-    n_q_heads] or None; workspace from alloc_chunk_workspace."""
+    n_q_heads] or None; workspace from alloc_chunk_workspace. (Single tokens without masks, cap or bias: qc_attend is faster.)"""
     dev, d, shape, dtype = ctx.device, ctx.d, q.shape, q.dtype
     if len(shape) != 3:
         raise ValueError(f"q is {tuple(shape)}, not [n_tokens, n_q_heads, {d}]")
