@@ -35,13 +35,16 @@
 // As M moves seldom, weights are made from scores at once, without a look for the largest first, and looked over afterwards;
 // where one passes the limit, or some place is not seen, that half is done again, step by step.
 //
-// What bounds it. Long chunks (4,096 tokens over 28,672, 32/8 heads of 128, int8, bf16: 1,830 us, 1.12 PFLOP/s, 59 % of a large
-// matrix product's rate) are bound by the softmax: a warp takes about 3,000 of a tile pair's cycles for its 32 x 128 scores, and the
-// way from weights through products to the next scores another 1,700; products alone take 0.95 ms, with the conversion 1.14. Two
-// CTAs apart, each with all of a tile's operands, are bound by shared memory instead. Single tokens (32 over windows of 4,096,
-// e2m1, capped: 332 us for 24 of memory) use one row in 256 of a tile: the cap's arithmetic in one warp and the conversion (about
-// 2,000 cycles a tile) follow one another. Short prompts (4 of up to 2,048 over 577: 106 us for 7) are starts, masked tiles
-// step by step, and ends.
+// What bounds it. Long chunks (4,096 tokens over 28,672, 32/8 heads of 128, int8, bf16: 1,810 us, 1.14 PFLOP/s, 60 % of a large
+// matrix product's rate; fp16, with two terms a weight, 2,150) are bound by no pipe: over 2,048 tokens and 8,192 places the issue
+// slots are 46 % busy, the tensor pipe 34, the integer pipe 30, the multiply-add pipe 26, the exponentials' 19. It is the chain
+// scores, weights, products, next scores: two row tiles in turn do not hide it (products alone take 0.95 ms, with the conversion
+// 1.14). Two CTAs apart, each with all of a tile's operands, are bound by shared memory instead. Single tokens (32 over windows
+// of 4,096, e2m1, capped: 329 to 352 us for 24 of memory) use one row in 256 of a tile, and a tile takes 2.9 us all the same, longer than
+// a full one of the long chunk (2.25): 19 % of the issue slots, warps waiting for loads; conversion and one warp's capped scores
+// follow one another. Short prompts (4 of up to 2,048 over 577: 114 us for 7) are starts, masked tiles step by step, and ends;
+// so are tiles of a last warp in which lanes have no row, since those count as the first token's. A job's own start and end
+// take 9.7 us where nothing else of the unit hides them (4,096 single tokens of empty contexts over 8 heads: 4.14 ms).
 #pragma once
 
 #include <math.h>
@@ -60,8 +63,9 @@ using namespace fq::sm100;
 static_assert(kTile == kChunkTile, "tiles of places");
 
 // One above this has its reference moved with the next tile. A move ahead of need costs a tile its rescaling, one in need the
-// step-by-step half besides: 4,096 tokens over 28,672 (int8, bf16) take 2,145 us when all moves wait for the limit, 2,080 with
-// 30,000 here, 1,949 with 8,192, 1,862 with 2,048, 1,825 with 512, 1,831 with 256.
+// step-by-step half besides: 4,096 tokens over 28,672 (int8, bf16, 128) took 2,145 us when all moves waited for the limit, 2,080 with
+// 30,000 here. With 8,192, 2,048, 512 and 128 they take 1,944, 1,845, 1,814 and 1,810; fp16's 2,294, 2,186, 2,157, 2,143; heads
+// of 64 (e4m3, fp16) 2,165, 2,045, 1,980, 1,958; windows of 4,096 429, 410, 397, 390; with a bias by distance 1,884 to 1,887.
 constexpr float kSoon = 512.f;
 constexpr float kMostLog = 15.9f, kMostP = 61147.f;     // the largest product that is let to fp16, and its log2
 constexpr float kTop = 4.f;              // a new reference puts the largest one at 2^kTop, or up to twice that

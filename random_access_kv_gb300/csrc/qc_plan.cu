@@ -4,7 +4,7 @@
 // page. Every block takes the sums of all requests by itself, ceil(n_seq / 1024) neighbouring requests a thread, so that
 // one launch does it without blocks that wait for one another; then the blocks share the tokens and the pages out. A
 // token finds its thread's run of requests by halving among 1,024 sums in shared memory, and its request by walking that
-// run. Bound by the launch: 3.8 us on the device for a decoding step (a call takes the host 8.6), 5.5 us for 512 prompts of up to
+// run. Bound by the launch: 3.8 us on the device for a decoding step (a call takes the host 8.6), 5.8 us for 512 prompts of up to
 // 1,024 tokens, whose 4.2 MB of slots and positions are 0.6 us of memory.
 #include "qc_internal.h"
 
